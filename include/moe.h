@@ -19,6 +19,14 @@
  *   moe_expert_gate_up_fp4 / moe_expert_down_fp4  the expert GEMMs with 4-bit weights
  *   moe_round_output     the combine's final rounding of an fp32 sum to bf16
  *   moe_router_stats     per-expert load, aux loss, z-loss, drops, imbalance
+ *   moe_route_grouped    top-k of given logits limited to the best groups of experts
+ *   moe_route_backward   gradient of gates, load-balancing loss and z-loss by the logits
+ *   moe_quantize_rows_i8 rows to 8-bit integers with a scale each (optionally dispatched)
+ *   moe_expert_gate_up_i8 / moe_expert_gate_up_gather_i8 / moe_expert_down_i8  the expert
+ *                        GEMMs over 8-bit rows and weights
+ *   moe_block_norm / moe_combine_norm  post-norm, gate, scaled residual and the next pre-norm
+ *                        (the second with the combine in front)
+ *   moe_block_norm_backward  their gradients
  *
  * Sources (web pages on Mixture-of-Experts, cited by title and section):
  *   [MoE-Explained]  "Hugging Face 图解 Mixture of Experts（MoE）原理、训练与推理权衡"
@@ -104,6 +112,11 @@ typedef enum {
   MOE_SELECT_UNIFORM = 0,       /* slot j of token t takes expert (t k + j) mod E        */
   MOE_SELECT_HASH = 1           /* k distinct experts from a hash of the token id         */
 } moe_select_rule;
+
+typedef enum {
+  MOE_GROUP_MAX = 0,            /* a group's value is its largest key                    */
+  MOE_GROUP_TOP2 = 1            /* ... the sum of its two largest scores (+ bias)         */
+} moe_group_score;
 
 /* Device error codes recorded by kernels (first one wins until read). */
 #define MOE_DEVERR_NONE 0
@@ -687,6 +700,173 @@ MOE_API moe_status moe_expert_down_fp4(const void* h, const int32_t* offsets, in
                      int32_t F, int64_t rows_max, const uint8_t* codes, const uint8_t* scales,
                      int32_t fmt, const float* tensor_scale, const float* gate_of_row,
                      int32_t y_dtype, void* y_rows, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * moe_route_grouped -- top-k limited to the best groups of experts.
+ * [Handbook-News] "真正难在三个环节" item 2 (a bias for balance that only selects), tweet
+ * (softmax / sigmoid / sqrt(softplus)); [MoE-Explained] section "什么是稀疏性？" (KeepTopK).
+ * The E experts form n_groups groups of n = E / n_groups neighbours.  An expert's key is
+ * its logit (no bias) or score + bias in fp64; a group's value is its largest key
+ * (MOE_GROUP_MAX) or the sum of its two largest scores, or scores + bias
+ * (MOE_GROUP_TOP2; in fp64; a single expert's alone).  The groups_kept groups of largest
+ * value are kept and the k largest keys of their experts are selected; ties go to the
+ * lower index, the order is key descending, then index ascending.
+ *   logits       (device) [T, E] fp32 (moe_router_logits)
+ *   select_bias  (device) [E] fp32 or NULL
+ *   score, renormalize, scale: as moe_route (the gates are taken in fp64 and rounded once)
+ *   topk_idx     (device) [T, k] int32 out;  topk_gate (device) [T, k] fp32 out
+ * A logit of -inf or NaN masks its expert: its key is -inf whatever its bias, it adds
+ * nothing to its group, and its gate is 0 where it is selected all the same (fewer than k
+ * unmasked experts in the kept groups); a token with every expert masked has gates 0.
+ * A logit of +inf counts as the largest float.
+ * Errors: INVALID_ARG for a null pointer, T < 0, k < 1, n_groups < 1, groups_kept outside
+ * [1, n_groups], E not a multiple of n_groups, k > groups_kept * n, an unknown score or
+ * group_score, renormalize not 0/1 or a non-finite scale; UNSUPPORTED for E > 1024, k > 32
+ * or n_groups > 32.
+ * ---------------------------------------------------------------------------------- */
+MOE_API moe_status moe_route_grouped(const float* logits, const float* select_bias, int32_t T, int32_t E,
+                     int32_t k, int32_t n_groups, int32_t groups_kept, int32_t group_score, int32_t score,
+                     int32_t renormalize, float scale, int32_t* topk_idx, float* topk_gate, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * moe_route_backward -- the gradient of a routing by its logits.
+ * [MoE-Explained] section "什么是稀疏性？" (gates), auxiliary load-balancing loss, section
+ * "使用路由器 Z-loss 稳定训练".  For whichever call selected the experts (moe_route,
+ * moe_route_grouped, moe_route_fixed); the selection itself has no gradient.
+ *   logits     (device) [T, E] fp32
+ *   topk_idx   (device) [T, k] int32 and d_gate (device) [T, k] fp32: the selection and the
+ *              gradient of its gates; both NULL: the loss terms alone (k is then ignored)
+ *   score, renormalize, scale: the routing's
+ *   load       (device) [E] fp32: f_e of moe_router_stats, or NULL when aux_coef is 0
+ *   aux_coef   adds aux_coef * d aux / d logits, aux = E sum_e f_e P_e (f held constant)
+ *   z_coef     adds z_coef * d z / d logits, z = mean_t lse_t^2
+ *   d_logits   (device) [T, E] fp32 out (overwritten); must not overlap the inputs
+ * A masked logit (-inf or NaN) has gradient 0.  An expert a token names twice takes the sum
+ * of both slots' gradients.  A topk_idx entry outside [0, E) records MOE_DEVERR_EXPERT_ID
+ * and its slot is left out.
+ * Errors: INVALID_ARG for a null logits or d_logits, one of topk_idx / d_gate without the
+ * other, aux_coef != 0 without load, T < 0, k < 1 or k > E with a selection, an unknown
+ * score, renormalize not 0/1 or a non-finite scale or coefficient; UNSUPPORTED for E > 1024
+ * or k > 32.
+ * ---------------------------------------------------------------------------------- */
+MOE_API moe_status moe_route_backward(const float* logits, const int32_t* topk_idx, const float* d_gate,
+                     int32_t T, int32_t E, int32_t k, int32_t score, int32_t renormalize, float scale,
+                     const float* load, float aux_coef, float z_coef, float* d_logits, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Expert GEMMs in 8-bit integers, with a scale for each row and each weight row.
+ * [Handbook-Digest] "已确认", bullet "量化与推理" (routed experts kept in few bits).
+ *
+ * moe_quantize_rows_i8 -- q = rint(x * f) to the nearest even with f = 127 * (1 / amax) in
+ *   fp32 (both steps rounded), amax the row's largest |x|, and scale = amax / 127.  A row of zeros, or with amax below
+ *   2^-120, has q = 0 and scale 0; a row with an infinity or NaN has q = 0 and a NaN scale,
+ *   so exactly its products are NaN.
+ *   Serves the activations of every step and, once at load time, the weights (a row is an
+ *   output channel).
+ *   x        (device) [rows, cols], x_dtype
+ *   row_of   (device) [rows, k] int32 or NULL.  NULL: q (device) int8 [rows, cols] and scale
+ *            (device) [rows] fp32 out.  Otherwise the dispatch is fused into it: token t's
+ *            bytes and scale go to rows row_of[t, j] of q [rows_max, cols] and scale
+ *            [rows_max], -1 skipped, an index >= rows_max skipped and recorded as
+ *            MOE_DEVERR_ROW (k and rows_max are ignored without row_of).
+ *   Errors: INVALID_ARG for a null pointer, negative sizes, k < 1 or an unknown dtype;
+ *   UNSUPPORTED for cols not a multiple of 16 or above 16384, k > 32, rows >= 2^31 or an
+ *   unaligned x or q.
+ *
+ * moe_expert_gate_up_i8 -- H = silu(g) * u, bf16, with g = acc * x_scale * w_scale and acc the
+ *   exact int32 sum of x_q . W_gu (u likewise with the up rows).
+ *   x_q      (device) [rows_max, d] int8;  x_scale (device) [rows_max] fp32
+ *   W_gu     (device) [E, 2F, d] int8 (gate rows, then up rows);  w_scale (device) [E, 2F] fp32
+ *   h        (device) [rows_max, F] bf16 out
+ *   Tile orientation as moe_gate_up_weight_major says.
+ * moe_expert_gate_up_gather_i8 -- the same rows read through token_of_row from x_q [T, d] and
+ *   x_scale [T] (weight-major tiles, whatever the group sizes).  A token index outside [0, T)
+ *   is recorded as MOE_DEVERR_ROW and row 0 is read in its place.
+ * moe_expert_down_i8 -- y_rows = gate_of_row * acc * h_scale * w_scale, fp32 or bf16.
+ *   h_q      (device) [rows_max, F] int8;  h_scale (device) [rows_max] fp32
+ *   W_dn     (device) [E, d, F] int8;  w_scale (device) [E, d] fp32
+ * offsets, rows_max, gate_of_row and y_dtype as the bf16 calls; rows at or beyond
+ * offsets[E] are not written.  A scale may be any float (a NaN spreads to its row or column).
+ * Errors: INVALID_ARG for a null pointer (gate_of_row may be), a negative size or a bad
+ * y_dtype; UNSUPPORTED for E > 1024, d or F not a multiple of 16 or outside [128, 16384],
+ * rows_max >= 2^31, an unaligned pointer, or a driver that encodes no tensor maps.
+ * ---------------------------------------------------------------------------------- */
+MOE_API moe_status moe_quantize_rows_i8(const void* x, int32_t x_dtype, int64_t rows, int32_t cols,
+                     const int32_t* row_of, int32_t k, int64_t rows_max, int8_t* q, float* scale,
+                     void* stream);
+MOE_API moe_status moe_expert_gate_up_i8(const int8_t* x_q, const float* x_scale, const int32_t* offsets,
+                     int32_t E, int32_t d, int32_t F, int64_t rows_max, const int8_t* W_gu,
+                     const float* w_scale, void* h, void* stream);
+MOE_API moe_status moe_expert_gate_up_gather_i8(const int8_t* x_q, const float* x_scale, int32_t T,
+                     const int32_t* token_of_row, const int32_t* offsets, int32_t E, int32_t d,
+                     int32_t F, int64_t rows_max, const int8_t* W_gu, const float* w_scale, void* h,
+                     void* stream);
+MOE_API moe_status moe_expert_down_i8(const int8_t* h_q, const float* h_scale, const int32_t* offsets,
+                     int32_t E, int32_t d, int32_t F, int64_t rows_max, const int8_t* W_dn,
+                     const float* w_scale, const float* gate_of_row, int32_t y_dtype, void* y_rows,
+                     void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * The norms before and after a block, fused with its gate and the scaled residual.
+ * [MoE-Explained] section "什么是混合专家模型" (the MoE layer in its transformer block).
+ *   b  = y, or with post_weight: post_weight * y / rms(y);   rms(v) = sqrt(mean v^2 + eps)
+ *   x' = alpha * residual + gate * b
+ *   n  = pre_weight * x' / rms(x')                           (the next block's input)
+ * in fp32, each output rounded once (n is taken from the unrounded x').
+ *
+ * moe_block_norm
+ *   residual    (device) [T, d] r_dtype
+ *   y           (device) [T, d] y_dtype, the block's output; NULL: x' = alpha * residual
+ *               (the first pre-norm of a model; post_weight and gate must then be NULL)
+ *   post_weight (device) [d] fp32 or NULL (no post-norm)
+ *   gate        (device) [gate_rows, d] fp32 or NULL (1).  gate_rows divides T; token t takes
+ *               row t / (T / gate_rows): 1 row for all, one per sequence, or one per token
+ *   pre_weight  (device) [d] fp32 or NULL (no n)
+ *   x_out       (device) [T, d] r_dtype out, or NULL; may be residual itself
+ *   n_out       (device) [T, d] n_dtype out; required with pre_weight
+ * moe_combine_norm -- the same with y = moe_combine's sum: the kept rows of the token in slot
+ *   order (times topk_gate, if given), plus shared_y, in fp32, not rounded in between.
+ *   y_rows (device) [rows_max, d], row_of [T, k], topk_gate [T, k] or NULL, shared_y [T, d] or
+ *   NULL: as moe_combine.  y_out (device) [T, d] rows_dtype out or NULL: the sum, rounded, as
+ *   moe_block_norm_backward takes it.
+ * Errors: INVALID_ARG for a null residual, neither output asked for, pre_weight and n_out not
+ * given together, post_weight or gate without y, gate_rows < 1 or not a divisor of T, eps not
+ * positive and finite, a non-finite alpha, a negative size or an unknown dtype; UNSUPPORTED for
+ * d not a multiple of 8 or above 8192, T >= 2^24, k > 32 or an unaligned pointer.
+ *
+ * moe_block_norm_backward -- gradients of moe_block_norm from its saved x_out and y.
+ *   d_x         (device) [T, d] r_dtype: gradient of x_out, or NULL (zero)
+ *   d_n         (device) [T, d] n_dtype: gradient of n_out; required with pre_weight
+ *   x_out       (device) [T, d] r_dtype; required with pre_weight
+ *   y           (device) [T, d] y_dtype or NULL, with post_weight, gate, gate_rows as above
+ *   d_residual  (device) [T, d] r_dtype out; may be d_x itself
+ *   d_y         (device) [T, d] y_dtype out; required with y
+ *   d_post_weight [d], d_gate [gate_rows, d], d_pre_weight [d] (device) fp32 out, each NULL or
+ *               its input given.  Column sums are fp32 per block of tokens, then fp64 in a fixed
+ *               order: results repeat bit for bit.
+ *   workspace   (device) >= moe_block_norm_backward_workspace_bytes(T, d, gate_rows), gate_rows
+ *               1 without a gate; calls that overlap need one each
+ * T = 0 clears the weight gradients.
+ * Errors: as above; INVALID_ARG also when a gradient is asked for without its input, or neither
+ * d_x nor d_n is given; WORKSPACE if too small.
+ * ---------------------------------------------------------------------------------- */
+MOE_API moe_status moe_block_norm(const void* residual, int32_t r_dtype, const void* y, int32_t y_dtype,
+                     const float* post_weight, const float* gate, int32_t gate_rows, float alpha,
+                     const float* pre_weight, float eps, int32_t T, int32_t d, void* x_out, void* n_out,
+                     int32_t n_dtype, void* stream);
+MOE_API moe_status moe_combine_norm(const void* residual, int32_t r_dtype, const void* y_rows,
+                     int32_t rows_dtype, const int32_t* row_of, const float* topk_gate,
+                     const void* shared_y, int32_t k, int64_t rows_max, const float* post_weight,
+                     const float* gate, int32_t gate_rows, float alpha, const float* pre_weight,
+                     float eps, int32_t T, int32_t d, void* y_out, void* x_out, void* n_out,
+                     int32_t n_dtype, void* stream);
+MOE_API size_t moe_block_norm_backward_workspace_bytes(int32_t T, int32_t d, int32_t gate_rows);
+MOE_API moe_status moe_block_norm_backward(const void* d_x, const void* d_n, const void* x_out, const void* y,
+                     int32_t r_dtype, int32_t n_dtype, int32_t y_dtype, const float* post_weight,
+                     const float* gate, int32_t gate_rows, float alpha, const float* pre_weight,
+                     float eps, int32_t T, int32_t d, void* d_residual, void* d_y, float* d_post_weight,
+                     float* d_gate, float* d_pre_weight, void* workspace, size_t workspace_bytes,
+                     void* stream);
 
 /* Largest workspace any of the calls above needs for these sizes, for every call with
  * at most T tokens (each size query covers the batches below its T). */

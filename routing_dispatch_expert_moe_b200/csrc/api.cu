@@ -38,6 +38,8 @@ namespace {
 constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
 constexpr long long kMaxT = 1LL << 24;
+constexpr int kMaxI8 = 16384;    // longest 8-bit row (its int32 sums stay below 2^28)
+constexpr int kMaxNorm = 8192;   // widest row of the block norms
 
 inline cudaStream_t S(void* s) { return static_cast<cudaStream_t>(s); }
 
@@ -561,6 +563,177 @@ moe_status moe_router_stats(const float* logits, const int32_t* counts, const in
   const size_t need = router_stats_workspace_bytes(T, E);
   if (T > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
   return launch_router_stats(logits, counts, kept, T, E, k, score, load, stats5, workspace, S(stream));
+}
+
+moe_status moe_route_grouped(const float* logits, const float* select_bias, int32_t T, int32_t E, int32_t k,
+                             int32_t n_groups, int32_t groups_kept, int32_t group_score, int32_t score,
+                             int32_t renormalize, float scale, int32_t* topk_idx, float* topk_gate, void* stream) {
+  if (T < 0 || E < 1 || k < 1 || n_groups < 1 || groups_kept < 1 || groups_kept > n_groups || E % n_groups != 0 ||
+      (long long)groups_kept * (E / n_groups) < k)
+    return MOE_ERR_INVALID_ARG;
+  if (score < MOE_SCORE_SOFTMAX || score > MOE_SCORE_SQRT_SOFTPLUS || (renormalize != 0 && renormalize != 1) ||
+      !isfinite(scale) || (group_score != MOE_GROUP_MAX && group_score != MOE_GROUP_TOP2))
+    return MOE_ERR_INVALID_ARG;
+  const moe_status st = check_dims(T, E, k);
+  if (st != MOE_OK) return st;
+  if (n_groups > 32) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !topk_gate) return MOE_ERR_INVALID_ARG;
+  return launch_route_grouped(logits, T, E, k, n_groups, groups_kept, group_score, score, renormalize, scale,
+                              select_bias, topk_idx, topk_gate, S(stream));
+}
+
+moe_status moe_route_backward(const float* logits, const int32_t* topk_idx, const float* d_gate, int32_t T, int32_t E,
+                              int32_t k, int32_t score, int32_t renormalize, float scale, const float* load,
+                              float aux_coef, float z_coef, float* d_logits, void* stream) {
+  if ((topk_idx == nullptr) != (d_gate == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!topk_idx) k = 1;
+  const moe_status st = check_dims(T, E, k);
+  if (st != MOE_OK) return st;
+  if (score < MOE_SCORE_SOFTMAX || score > MOE_SCORE_SQRT_SOFTPLUS || (renormalize != 0 && renormalize != 1) ||
+      !isfinite(scale) || !isfinite(aux_coef) || !isfinite(z_coef))
+    return MOE_ERR_INVALID_ARG;
+  if (aux_coef != 0.f && !load) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!logits || !d_logits) return MOE_ERR_INVALID_ARG;
+  return launch_route_backward(logits, topk_idx, d_gate, T, E, k, score, renormalize, scale, load, aux_coef, z_coef,
+                               d_logits, S(stream));
+}
+
+moe_status moe_quantize_rows_i8(const void* x, int32_t x_dtype, int64_t rows, int32_t cols, const int32_t* row_of,
+                                int32_t k, int64_t rows_max, int8_t* q, float* scale, void* stream) {
+  if (rows < 0 || cols < 1 || !dtype_ok(x_dtype) || (row_of && (k < 1 || rows_max < 0))) return MOE_ERR_INVALID_ARG;
+  if (cols % 16 != 0 || cols > kMaxI8 || rows >= (1LL << 31) || (row_of && k > kMaxK)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || ((!row_of || rows_max > 0) && (!q || !scale))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q)) return MOE_ERR_UNSUPPORTED;
+  return launch_quantize_rows_i8(x, x_dtype, rows, cols, row_of, k, rows_max, q, scale, S(stream));
+}
+
+static moe_status check_i8(const int8_t* a, const float* a_scale, const int32_t* offsets, int32_t E, int32_t d,
+                           int32_t F, int64_t rows_max, const int8_t* W, const float* w_scale, const void* out) {
+  if (E < 1 || d < 1 || F < 1 || rows_max < 0) return MOE_ERR_INVALID_ARG;
+  if (E > kMaxE || d % 16 != 0 || F % 16 != 0 || d < 128 || F < 128 || d > kMaxI8 || F > kMaxI8 ||
+      rows_max >= (1LL << 31))
+    return MOE_ERR_UNSUPPORTED;
+  if (!offsets || !W || !w_scale) return MOE_ERR_INVALID_ARG;
+  if (rows_max > 0 && (!a || !a_scale || !out)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(W) || !aligned16(w_scale) || !aligned16(out)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_expert_gate_up_i8(const int8_t* x_q, const float* x_scale, const int32_t* offsets, int32_t E, int32_t d,
+                                 int32_t F, int64_t rows_max, const int8_t* W_gu, const float* w_scale, void* h,
+                                 void* stream) {
+  const moe_status st = check_i8(x_q, x_scale, offsets, E, d, F, rows_max, W_gu, w_scale, h);
+  if (st != MOE_OK || rows_max == 0) return st;
+  return launch_gate_up_i8(x_q, x_scale, offsets, E, d, F, rows_max, W_gu, w_scale, h, S(stream));
+}
+
+moe_status moe_expert_gate_up_gather_i8(const int8_t* x_q, const float* x_scale, int32_t T,
+                                        const int32_t* token_of_row, const int32_t* offsets, int32_t E, int32_t d,
+                                        int32_t F, int64_t rows_max, const int8_t* W_gu, const float* w_scale,
+                                        void* h, void* stream) {
+  if (T < 0) return MOE_ERR_INVALID_ARG;
+  if ((long long)T >= kMaxT) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) rows_max = 0;                                  // no token: no row
+  const moe_status st = check_i8(x_q, x_scale, offsets, E, d, F, rows_max, W_gu, w_scale, h);
+  if (st != MOE_OK || rows_max == 0) return st;
+  if (!token_of_row) return MOE_ERR_INVALID_ARG;
+  return launch_gate_up_gather_i8(x_q, x_scale, token_of_row, T, offsets, E, d, F, rows_max, W_gu, w_scale, h,
+                                  S(stream));
+}
+
+moe_status moe_expert_down_i8(const int8_t* h_q, const float* h_scale, const int32_t* offsets, int32_t E, int32_t d,
+                              int32_t F, int64_t rows_max, const int8_t* W_dn, const float* w_scale,
+                              const float* gate_of_row, int32_t y_dtype, void* y_rows, void* stream) {
+  if (!dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARG;
+  const moe_status st = check_i8(h_q, h_scale, offsets, E, d, F, rows_max, W_dn, w_scale, y_rows);
+  if (st != MOE_OK || rows_max == 0) return st;
+  return launch_down_i8(h_q, h_scale, offsets, E, d, F, rows_max, W_dn, w_scale, gate_of_row, y_dtype, y_rows,
+                        S(stream));
+}
+
+// Sizes, dtypes and scalars of the block norms; gate_rows counts as 1 without a gate.
+static moe_status check_norm(int32_t r_dtype, int32_t y_dtype, int32_t n_dtype, const float* gate, int32_t gate_rows,
+                             float alpha, float eps, int32_t T, int32_t d) {
+  if (T < 0 || d < 1 || !dtype_ok(r_dtype) || !dtype_ok(y_dtype) || !dtype_ok(n_dtype) || !isfinite(alpha) ||
+      !isfinite(eps) || !(eps > 0.f))
+    return MOE_ERR_INVALID_ARG;
+  if (gate && (gate_rows < 1 || T % gate_rows != 0)) return MOE_ERR_INVALID_ARG;
+  if (d % 8 != 0 || d > kMaxNorm || (long long)T >= kMaxT) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_block_norm(const void* residual, int32_t r_dtype, const void* y, int32_t y_dtype,
+                          const float* post_weight, const float* gate, int32_t gate_rows, float alpha,
+                          const float* pre_weight, float eps, int32_t T, int32_t d, void* x_out, void* n_out,
+                          int32_t n_dtype, void* stream) {
+  const moe_status st = check_norm(r_dtype, y_dtype, n_dtype, gate, gate_rows, alpha, eps, T, d);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!y && (post_weight || gate)) return MOE_ERR_INVALID_ARG;
+  if (!residual || (pre_weight == nullptr) != (n_out == nullptr) || (!x_out && !n_out)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(residual) || !aligned16(y) || !aligned16(post_weight) || !aligned16(gate) || !aligned16(pre_weight) ||
+      !aligned16(x_out) || !aligned16(n_out))
+    return MOE_ERR_UNSUPPORTED;
+  return launch_block_norm(residual, r_dtype, y, y_dtype, nullptr, nullptr, nullptr, 0, 0, nullptr, post_weight, gate,
+                           gate_rows, alpha, pre_weight, eps, T, d, x_out, n_out, n_dtype, S(stream));
+}
+
+moe_status moe_combine_norm(const void* residual, int32_t r_dtype, const void* y_rows, int32_t rows_dtype,
+                            const int32_t* row_of, const float* topk_gate, const void* shared_y, int32_t k,
+                            int64_t rows_max, const float* post_weight, const float* gate, int32_t gate_rows,
+                            float alpha, const float* pre_weight, float eps, int32_t T, int32_t d, void* y_out,
+                            void* x_out, void* n_out, int32_t n_dtype, void* stream) {
+  const moe_status st = check_norm(r_dtype, rows_dtype, n_dtype, gate, gate_rows, alpha, eps, T, d);
+  if (st != MOE_OK) return st;
+  if (k < 1 || rows_max < 0) return MOE_ERR_INVALID_ARG;
+  if (k > kMaxK) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!residual || !row_of || (rows_max > 0 && !y_rows) || (pre_weight == nullptr) != (n_out == nullptr) ||
+      (!x_out && !n_out))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(residual) || !aligned16(y_rows) || !aligned16(shared_y) || !aligned16(post_weight) ||
+      !aligned16(gate) || !aligned16(pre_weight) || !aligned16(y_out) || !aligned16(x_out) || !aligned16(n_out))
+    return MOE_ERR_UNSUPPORTED;
+  return launch_block_norm(residual, r_dtype, y_rows, rows_dtype, row_of, topk_gate, shared_y, k, rows_max, y_out,
+                           post_weight, gate, gate_rows, alpha, pre_weight, eps, T, d, x_out, n_out, n_dtype,
+                           S(stream));
+}
+
+size_t moe_block_norm_backward_workspace_bytes(int32_t T, int32_t d, int32_t gate_rows) {
+  if (T < 1 || d < 1 || gate_rows < 1 || T % gate_rows != 0) return 0;
+  return block_norm_grad_workspace_bytes(T, d, gate_rows);
+}
+
+moe_status moe_block_norm_backward(const void* d_x, const void* d_n, const void* x_out, const void* y, int32_t r_dtype,
+                                   int32_t n_dtype, int32_t y_dtype, const float* post_weight, const float* gate,
+                                   int32_t gate_rows, float alpha, const float* pre_weight, float eps, int32_t T,
+                                   int32_t d, void* d_residual, void* d_y, float* d_post_weight, float* d_gate,
+                                   float* d_pre_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  moe_status st = check_norm(r_dtype, y_dtype, n_dtype, gate, gate_rows, alpha, eps, T, d);
+  if (st != MOE_OK) return st;
+  if ((d_post_weight && !post_weight) || (d_gate && !gate) || (d_pre_weight && !pre_weight)) return MOE_ERR_INVALID_ARG;
+  if (!gate) gate_rows = 1;
+  if (T == 0) {
+    const size_t row = (size_t)d * sizeof(float);
+    if (d_post_weight) st = cuda_status(cudaMemsetAsync(d_post_weight, 0, row, S(stream)));
+    if (st == MOE_OK && d_gate) st = cuda_status(cudaMemsetAsync(d_gate, 0, row * gate_rows, S(stream)));
+    if (st == MOE_OK && d_pre_weight) st = cuda_status(cudaMemsetAsync(d_pre_weight, 0, row, S(stream)));
+    return st;
+  }
+  if (!y && (post_weight || gate || d_y)) return MOE_ERR_INVALID_ARG;
+  if ((y && !d_y) || !d_residual || (!d_x && !d_n)) return MOE_ERR_INVALID_ARG;
+  if ((pre_weight == nullptr) != (d_n == nullptr) || (pre_weight && !x_out)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(d_x) || !aligned16(d_n) || !aligned16(x_out) || !aligned16(y) || !aligned16(post_weight) ||
+      !aligned16(gate) || !aligned16(pre_weight) || !aligned16(d_residual) || !aligned16(d_y) || !aligned16(d_gate) ||
+      !aligned16(workspace))
+    return MOE_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < block_norm_grad_workspace_bytes(T, d, gate_rows)) return MOE_ERR_WORKSPACE;
+  return launch_block_norm_backward(d_x, d_n, x_out, y, y_dtype, r_dtype, n_dtype, post_weight, gate, gate_rows, alpha,
+                                    pre_weight, eps, T, d, d_residual, d_y, d_post_weight, d_gate, d_pre_weight,
+                                    workspace, S(stream));
 }
 
 size_t moe_workspace_bytes(int32_t T, int32_t d, int32_t E, int32_t k) {

@@ -257,4 +257,40 @@ moe_status launch_down_tc(const void* h, const int32_t* offsets, int E, int d, i
                           long long rows_max, const void* W_dn, const float* gate_of_row,
                           int y_dtype, void* y_rows, cudaStream_t s);
 
+// Group-limited routing and a routing's gradient (route_group.cu, route_grad.cu).
+moe_status launch_route_grouped(const float* logits, int T, int E, int k, int n_groups, int groups_kept,
+                                int group_score, int score, int renorm, float scale, const float* bias,
+                                int32_t* topk_idx, float* topk_gate, cudaStream_t s);
+moe_status launch_route_backward(const float* logits, const int32_t* topk_idx, const float* d_gate, int T, int E,
+                                 int k, int score, int renorm, float scale, const float* load, float aux_coef,
+                                 float z_coef, float* d_logits, cudaStream_t s);
+
+// 8-bit rows (quant_i8.cu) and the expert GEMMs over them (ffn_tc.cu, ffn_wm.cu).
+moe_status launch_quantize_rows_i8(const void* x, int dtype, long long rows, int cols, const int32_t* row_of, int k,
+                                   long long rows_max, int8_t* q, float* scale, cudaStream_t s);
+moe_status launch_gate_up_i8(const int8_t* x_q, const float* x_scale, const int32_t* offsets, int E, int d, int F,
+                             long long rows_max, const int8_t* W, const float* w_scale, void* h, cudaStream_t s);
+moe_status launch_gate_up_wm_i8(const int8_t* x_q, const float* x_scale, const int32_t* offsets, int E, int d, int F,
+                                long long rows_max, const int8_t* W, const float* w_scale, void* h, cudaStream_t s);
+moe_status launch_gate_up_gather_i8(const int8_t* x_q, const float* x_scale, const int32_t* token_of_row, int T,
+                                    const int32_t* offsets, int E, int d, int F, long long rows_max, const int8_t* W,
+                                    const float* w_scale, void* h, cudaStream_t s);
+moe_status launch_down_i8(const int8_t* h_q, const float* h_scale, const int32_t* offsets, int E, int d, int F,
+                          long long rows_max, const int8_t* W, const float* w_scale, const float* gate_of_row,
+                          int y_dtype, void* y_rows, cudaStream_t s);
+moe_status launch_down_wm_i8(const int8_t* h_q, const float* h_scale, const int32_t* offsets, int E, int d, int F,
+                             long long rows_max, const int8_t* W, const float* w_scale, const float* gate_of_row,
+                             int y_dtype, void* y_rows, cudaStream_t s);
+
+// The norms around a block (block_norm.cu); row_of non-null: y holds expert rows to combine.
+moe_status launch_block_norm(const void* r, int r_dtype, const void* y, int y_dtype, const int32_t* row_of,
+                             const float* topk_gate, const void* shared_y, int k, long long rows_max, void* y_out,
+                             const float* post, const float* gate, int G, float alpha, const float* pre, float eps,
+                             int T, int d, void* x_out, void* n_out, int n_dtype, cudaStream_t s);
+size_t block_norm_grad_workspace_bytes(int T, int d, int G);
+moe_status launch_block_norm_backward(const void* d_x, const void* d_n, const void* x_out, const void* y, int y_dtype,
+                                      int r_dtype, int n_dtype, const float* post, const float* gate, int G,
+                                      float alpha, const float* pre, float eps, int T, int d, void* d_r, void* d_y,
+                                      float* d_post, float* d_gate, float* d_pre, void* ws, cudaStream_t s);
+
 }  // namespace moe

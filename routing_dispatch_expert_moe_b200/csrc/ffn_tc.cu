@@ -110,6 +110,28 @@ __device__ __forceinline__ void stage_red32(uint8_t* stage, const float (&v)[32]
   __syncwarp();
 }
 
+// Four column scales from column col of n (a multiple of 16, as col is of 4); 0 past the end.
+// Every lane reads the same address.
+__device__ __forceinline__ void col_scale4(const float* __restrict__ w, int col, int n, float (&f)[4]) {
+  const float4 q = col < n ? __ldg(reinterpret_cast<const float4*>(w + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
+}
+// 32 accumulators of a row times the row's factor (I8: and their column scales).
+template <bool I8>
+__device__ __forceinline__ void scaled32(const uint32_t (&v)[32], float gs, const float* __restrict__ w_scale, int col,
+                                         int n, float (&y)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if constexpr (I8) {
+      float s[4];
+      col_scale4(w_scale, col + (i & ~3), n, s);
+      y[i] = acc_value<true>(v[i]) * gs * s[i & 3];
+    } else {
+      y[i] = __uint_as_float(v[i]) * gs;
+    }
+  }
+}
+
 // OutT: element type of the output rows (MODE 0 always writes bf16 H; MODE 1 writes
 // bf16 or fp32 gated rows; MODE 3 adds into fp32 token rows).
 // One tile's epilogue for one warp: its 32 accumulator rows (TMEM lanes at taddr) become
@@ -118,12 +140,14 @@ __device__ __forceinline__ void stage_red32(uint8_t* stage, const float (&v)[32]
 //   MODE 0: columns [0,128) gate, [128,256) up -> H = silu(g) * u for features n_tile*128 + ...
 //   MODE 1: 256 columns -> gate_of_row[row] * acc for outputs n_tile*256 + ...
 // MODE 1 / 3 process the 32-column chunks [c_begin, c_end) of the 256 (a warp may own half).
-template <int MODE, typename OutT>
+// I8: the accumulators are int32 sums of 8-bit products; gs carries the row's scale (times its
+// gate in MODE 1), and w_scale points to the expert's column scales (gate columns, then up).
+template <int MODE, typename OutT, bool I8 = false>
 __device__ __forceinline__ void epilogue_tile(uint32_t taddr, uint8_t* stage, int lane, long long wrow0, int wrows,
                                               int n_tile, int F, int N_out, const float* __restrict__ gate_of_row,
                                               OutT* __restrict__ out, const int32_t* __restrict__ token_of_row,
                                               int n_tokens, int* err, float gs, int c_begin = 0,
-                                              int c_end = BN / 32) {
+                                              int c_end = BN / 32, const float* __restrict__ w_scale = nullptr) {
   if constexpr (MODE == 3) {
     const int n0 = n_tile * BN;
     const uint64_t pol = l2_evict_last_policy();
@@ -159,10 +183,20 @@ __device__ __forceinline__ void epilogue_tile(uint32_t taddr, uint8_t* stage, in
       float h[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float gi = __uint_as_float(g[i]);
+        float gi, ui;
+        if constexpr (I8) {
+          float sg[4], su[4];
+          col_scale4(w_scale, f0 + c * 32 + (i & ~3), F, sg);
+          col_scale4(w_scale + F, f0 + c * 32 + (i & ~3), F, su);
+          gi = acc_value<true>(g[i]) * (gs * sg[i & 3]);
+          ui = acc_value<true>(u[i]) * (gs * su[i & 3]);
+        } else {
+          gi = __uint_as_float(g[i]);
+          ui = __uint_as_float(u[i]);
+        }
         // fast exp / divide: H is rounded to bf16 next, far coarser than their error; the
         // exact forms made this epilogue the bound of the gate/up GEMM
-        h[i] = __fdividef(gi, 1.f + __expf(-gi)) * __uint_as_float(u[i]);
+        h[i] = __fdividef(gi, 1.f + __expf(-gi)) * ui;
       }
       stage_store32<OutT>(stage, h, lane, out, wrow0, wrows, F, f0 + c * 32, F);
     }
@@ -181,12 +215,10 @@ __device__ __forceinline__ void epilogue_tile(uint32_t taddr, uint8_t* stage, in
       tmem_regs_ready(va);
       tmem_regs_ready(vb);
       float y[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(va[i]) * gs;
+      scaled32<I8>(va, gs, w_scale, n0 + c * 32, N_out, y);
       stage_store32<OutT>(stage, y, lane, out, wrow0, wrows, N_out, n0 + c * 32, N_out);
       if (two) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(vb[i]) * gs;
+        scaled32<I8>(vb, gs, w_scale, n0 + (c + 1) * 32, N_out, y);
         stage_store32<OutT>(stage, y, lane, out, wrow0, wrows, N_out, n0 + (c + 1) * 32, N_out);
       }
     }
@@ -271,13 +303,14 @@ __device__ __forceinline__ void gather_producer(const CUtensorMap* tmB, uint32_t
   }
 }
 
-template <int MODE, typename OutT>
+template <int MODE, typename OutT, bool I8 = false>
 __global__ void __launch_bounds__(kThreadsTC, 1)
 grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const int32_t* __restrict__ offsets, int E, int K, int N_out, int F,
                        long long rows_max, const float* __restrict__ gate_of_row,
                        OutT* __restrict__ out, const int32_t* __restrict__ token_of_row, int n_tokens,
-                       const __nv_bfloat16* __restrict__ a_gather, int* err) {
+                       const __nv_bfloat16* __restrict__ a_gather, int* err, const float* __restrict__ row_scale,
+                       const float* __restrict__ w_scale) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -383,8 +416,7 @@ grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
           const uint64_t bdesc = sw128_desc(sb + L::b + stage * B_STAGE);
 #pragma unroll
           for (int kk = 0; kk < BK / UMMA_K; ++kk)   // +32 bytes along K per step (>> 4 = 2)
-            umma_bf16(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, make_idesc(BM, BN),
-                      (kb | kk) != 0 ? 1u : 0u);
+            umma<I8>(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, make_idesc_of<I8>(BM, BN), (kb | kk) != 0 ? 1u : 0u);
           umma_commit(bar_empty + 8 * stage);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -408,8 +440,9 @@ grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
       const long long wrow0 = (long long)tc.row0 + q * 32;          // first row of this warp
       const int wrows = min(32, max(0, tc.rows - q * 32));          // valid rows of this warp
       // the row's gate, fetched while the tile's MMAs still run
-      const float gs = ((MODE == 1 || MODE == 3) && lane < wrows && gate_of_row) ? __ldg(gate_of_row + wrow0 + lane)
-                                                                                  : 1.f;
+      float gs = ((MODE == 1 || MODE == 3) && lane < wrows && gate_of_row) ? __ldg(gate_of_row + wrow0 + lane) : 1.f;
+      if (I8) gs *= lane < wrows ? __ldg(row_scale + wrow0 + lane) : 0.f;
+      const float* ws = I8 ? w_scale + (long long)tc.e * (MODE == 0 ? 2 * F : N_out) : nullptr;
       const bool got = mbar_wait(bar_tfull + 8 * acc, acc_phase, abort_flag, err);
       // tcgen05.ld is .sync.aligned: the whole warp goes on, or the whole warp stops
       if (!__all_sync(0xffffffffu, got)) break;
@@ -419,8 +452,8 @@ grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
       (void)r_in;
       // a warp past the group's last row has nothing to read or store (warp-uniform)
       if (wrows > 0)
-        epilogue_tile<MODE, OutT>(taddr, stage, lane, wrow0, wrows, tc.n_tile, F, N_out, gate_of_row, out,
-                                  token_of_row, n_tokens, err, gs);
+        epilogue_tile<MODE, OutT, I8>(taddr, stage, lane, wrow0, wrows, tc.n_tile, F, N_out, gate_of_row, out,
+                                      token_of_row, n_tokens, err, gs, 0, BN / 32, ws);
       tc_fence_before();
       mbar_arrive(bar_tempty + 8 * acc);
     }
@@ -469,13 +502,13 @@ struct PairCfg {
   static_assert(smem <= 232448, "shared memory per CTA");
 };
 
-template <int MODE, typename OutT, bool WIDE>
+template <int MODE, typename OutT, bool WIDE, bool I8 = false>
 __global__ void __launch_bounds__(PairCfg<WIDE>::threads, 1)
 grouped_gemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const int32_t* __restrict__ offsets, int E, int K, int N_out, int F,
                         long long rows_max, const float* __restrict__ gate_of_row,
                         OutT* __restrict__ out, const int32_t* __restrict__ token_of_row, int n_tokens,
-                       int* err) {
+                        int* err, const float* __restrict__ row_scale, const float* __restrict__ w_scale) {
   using C = PairCfg<WIDE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -576,7 +609,8 @@ grouped_gemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
           const uint64_t bdesc = sw128_desc(sb + C::b + stage * B2_STAGE);
 #pragma unroll
           for (int kk = 0; kk < BK / UMMA_K; ++kk)
-            umma_bf16_pair(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, make_idesc(2 * BM, BN), (kb | kk) != 0 ? 1u : 0u);
+            umma_pair<I8>(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, make_idesc_of<I8>(2 * BM, BN),
+                          (kb | kk) != 0 ? 1u : 0u);
           umma_commit_pair_both(bar_empty + 8 * stage);
           if (++stage == C::stages) { stage = 0; phase ^= 1u; }
         }
@@ -602,8 +636,9 @@ grouped_gemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
       const long long wrow0 = (long long)tc.row0 + (int)rank * BM + q * 32;
       const int wrows = min(32, max(0, cta_rows - q * 32));
       // the row's gate, fetched while the tile's MMAs still run
-      const float gs = ((MODE == 1 || MODE == 3) && lane < wrows && gate_of_row) ? __ldg(gate_of_row + wrow0 + lane)
-                                                                                  : 1.f;
+      float gs = ((MODE == 1 || MODE == 3) && lane < wrows && gate_of_row) ? __ldg(gate_of_row + wrow0 + lane) : 1.f;
+      if (I8) gs *= lane < wrows ? __ldg(row_scale + wrow0 + lane) : 0.f;
+      const float* ws = I8 ? w_scale + (long long)tc.e * (MODE == 0 ? 2 * F : N_out) : nullptr;
       const bool got = mbar_wait(bar_tfull + 8 * acc, acc_phase, abort_flag, err);
       if (!__all_sync(0xffffffffu, got)) break;
       __syncwarp();
@@ -612,8 +647,8 @@ grouped_gemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
       // a warp past the group's last row has nothing to read or store (warp-uniform): with
       // many small groups most of a 256-row tile is padding
       if (wrows > 0)
-        epilogue_tile<MODE, OutT>(taddr, stage, lane, wrow0, wrows, tc.n_tile, F, N_out, gate_of_row, out,
-                                  token_of_row, n_tokens, err, gs, c_begin, c_end);
+        epilogue_tile<MODE, OutT, I8>(taddr, stage, lane, wrow0, wrows, tc.n_tile, F, N_out, gate_of_row, out,
+                                      token_of_row, n_tokens, err, gs, c_begin, c_end, ws);
       tc_fence_before();
       mbar_arrive_remote(map_to_rank(bar_tempty + 8 * acc, 0));
     }
@@ -627,22 +662,23 @@ grouped_gemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
   }
 }
 
-template <int MODE, typename OutT>
+template <int MODE, typename OutT, bool I8 = false>
 moe_status launch_tc(const CUtensorMap& ma, const CUtensorMap& mb, const int32_t* offsets, int E, int K, int N_out,
                      int F, long long rows_max, const float* gate_of_row, void* out, cudaStream_t s,
                      const int32_t* token_of_row = nullptr, int n_tokens = 0,
-                     const __nv_bfloat16* a_gather = nullptr) {
+                     const __nv_bfloat16* a_gather = nullptr, const float* row_scale = nullptr,
+                     const float* w_scale = nullptr) {
   static std::atomic<int> configured[kMaxDevices];
-  const moe_status st = ensure_smem_limit(configured, grouped_gemm_tc_kernel<MODE, OutT>, kSmemBytes);
+  const moe_status st = ensure_smem_limit(configured, grouped_gemm_tc_kernel<MODE, OutT, I8>, kSmemBytes);
   if (st != MOE_OK) return st;
   const int n_tiles = n_tiles_of<MODE>(F, N_out);
   const long long max_tiles = ((rows_max + BM - 1) / BM + E) * (long long)n_tiles;
   int grid = num_sms();
   if (max_tiles < grid) grid = (int)max_tiles;
   if (grid < 1) grid = 1;
-  grouped_gemm_tc_kernel<MODE, OutT><<<grid, kThreadsTC, kSmemBytes, s>>>(
+  grouped_gemm_tc_kernel<MODE, OutT, I8><<<grid, kThreadsTC, kSmemBytes, s>>>(
       ma, mb, offsets, E, K, N_out, F, rows_max, gate_of_row, static_cast<OutT*>(out), token_of_row, n_tokens,
-      a_gather, err_ptr());
+      a_gather, err_ptr(), row_scale, w_scale);
   return check_launch();
 }
 
@@ -667,13 +703,14 @@ static bool use_pairs(long long rows_max, int groups) {
   return groups > 0 && rows_max / groups >= kPairRowsMin;
 }
 
-template <int MODE, typename OutT, bool WIDE = false>
+template <int MODE, typename OutT, bool WIDE = false, bool I8 = false>
 moe_status launch_tc2(const CUtensorMap& ma, const CUtensorMap& mb, const int32_t* offsets, int E, int K, int N_out,
                       int F, long long rows_max, const float* gate_of_row, void* out, cudaStream_t s,
-                      const int32_t* token_of_row = nullptr, int n_tokens = 0) {
+                      const int32_t* token_of_row = nullptr, int n_tokens = 0, const float* row_scale = nullptr,
+                      const float* w_scale = nullptr) {
   static std::atomic<int> configured[kMaxDevices];
   const moe_status st =
-      ensure_smem_limit(configured, grouped_gemm_tc2_kernel<MODE, OutT, WIDE>, PairCfg<WIDE>::smem);
+      ensure_smem_limit(configured, grouped_gemm_tc2_kernel<MODE, OutT, WIDE, I8>, PairCfg<WIDE>::smem);
   if (st != MOE_OK) return st;
   const int n_tiles = n_tiles_of<MODE>(F, N_out);
   const long long max_tiles = ((rows_max + 2 * BM - 1) / (2 * BM) + E) * (long long)n_tiles;
@@ -692,9 +729,9 @@ moe_status launch_tc2(const CUtensorMap& ma, const CUtensorMap& mb, const int32_
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, grouped_gemm_tc2_kernel<MODE, OutT, WIDE>, ma, mb, offsets, E, K, N_out, F,
-                                        rows_max, gate_of_row, static_cast<OutT*>(out), token_of_row, n_tokens,
-                                        err_ptr()));
+  return cuda_status(cudaLaunchKernelEx(&cfg, grouped_gemm_tc2_kernel<MODE, OutT, WIDE, I8>, ma, mb, offsets, E, K,
+                                        N_out, F, rows_max, gate_of_row, static_cast<OutT*>(out), token_of_row,
+                                        n_tokens, err_ptr(), row_scale, w_scale));
 }
 
 // Token-major tiles (this file) pay off when the groups are large: a 256-row tile is then
@@ -790,6 +827,53 @@ moe_status launch_gate_up_gather_tc(const void* x, const int32_t* token_of_row, 
   if (!make_map(&mb, W_gu, (unsigned long long)E * 2 * F, d, 128)) return MOE_ERR_UNSUPPORTED;
   return launch_tc<4, __nv_bfloat16>(mb, mb, offsets, E, d, F, F, rows_max, nullptr, h, s, token_of_row, T,
                                      static_cast<const __nv_bfloat16*>(x));
+}
+
+// ---- 8-bit operands: x_q or h_q [rows_max, K] and the weights [E][N][K] are signed bytes, read by
+// the same tiles as rows of K / 2 two-byte elements (K a multiple of 16); the accumulators are
+// exact int32 sums and the epilogue multiplies them by the row's and the column's scale. ----
+moe_status launch_gate_up_i8(const int8_t* x_q, const float* x_scale, const int32_t* offsets, int E, int d, int F,
+                             long long rows_max, const int8_t* W, const float* w_scale, void* h, cudaStream_t s) {
+  if (prefer_weight_major(rows_max, E, false))
+    return launch_gate_up_wm_i8(x_q, x_scale, offsets, E, d, F, rows_max, W, w_scale, h, s);
+  const int K = d / 2;
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, x_q, (unsigned long long)rows_max, K, BM)) return MOE_ERR_UNSUPPORTED;
+  if (!make_map(&mb, W, (unsigned long long)E * 2 * F, K, 128)) return MOE_ERR_UNSUPPORTED;
+  if (use_pairs(rows_max, E))
+    return launch_tc2<0, __nv_bfloat16, false, true>(ma, mb, offsets, E, K, F, F, rows_max, nullptr, h, s, nullptr, 0,
+                                                     x_scale, w_scale);
+  return launch_tc<0, __nv_bfloat16, true>(ma, mb, offsets, E, K, F, F, rows_max, nullptr, h, s, nullptr, 0, nullptr,
+                                           x_scale, w_scale);
+}
+
+moe_status launch_down_i8(const int8_t* h_q, const float* h_scale, const int32_t* offsets, int E, int d, int F,
+                          long long rows_max, const int8_t* W, const float* w_scale, const float* gate_of_row,
+                          int y_dtype, void* y_rows, cudaStream_t s) {
+  if (prefer_weight_major(rows_max, E, true))
+    return launch_down_wm_i8(h_q, h_scale, offsets, E, d, F, rows_max, W, w_scale, gate_of_row, y_dtype, y_rows, s);
+  const int K = F / 2;
+  const bool pair = use_pairs(rows_max, E);
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, h_q, (unsigned long long)rows_max, K, BM)) return MOE_ERR_UNSUPPORTED;
+  if (!make_map(&mb, W, (unsigned long long)E * d, K, pair ? BM : BN)) return MOE_ERR_UNSUPPORTED;
+#define MOE_PAIR(T, WIDE)                                                                                        \
+  return launch_tc2<1, T, WIDE, true>(ma, mb, offsets, E, K, d, F, rows_max, gate_of_row, y_rows, s, nullptr, 0, \
+                                      h_scale, w_scale)
+  if (pair && K <= kWideMaxK) {
+    if (y_dtype == MOE_F32) MOE_PAIR(float, true);
+    MOE_PAIR(__nv_bfloat16, true);
+  }
+  if (pair) {
+    if (y_dtype == MOE_F32) MOE_PAIR(float, false);
+    MOE_PAIR(__nv_bfloat16, false);
+  }
+#undef MOE_PAIR
+  if (y_dtype == MOE_F32)
+    return launch_tc<1, float, true>(ma, mb, offsets, E, K, d, F, rows_max, gate_of_row, y_rows, s, nullptr, 0,
+                                     nullptr, h_scale, w_scale);
+  return launch_tc<1, __nv_bfloat16, true>(ma, mb, offsets, E, K, d, F, rows_max, gate_of_row, y_rows, s, nullptr, 0,
+                                           nullptr, h_scale, w_scale);
 }
 
 }  // namespace moe

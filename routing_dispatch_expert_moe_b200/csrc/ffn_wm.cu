@@ -119,6 +119,18 @@ __device__ __forceinline__ float wm_gate(const float* __restrict__ gate_of_row, 
   return (gate_of_row && r < tc.rows) ? __ldg(gate_of_row + tc.row0 + r) : 1.f;
 }
 
+// Scale of the row in place c * 32 + lane of a tile of 8-bit rows (0 past the tile's rows); with
+// token_of_row the scales are the tokens'.
+__device__ __forceinline__ float wm_row_scale(const float* __restrict__ row_scale,
+                                              const int32_t* __restrict__ token_of_row, int n_tokens,
+                                              const TileCoord& tc, int c, int lane) {
+  const int r = c * 32 + lane;
+  if (r >= tc.rows) return 0.f;
+  if (!token_of_row) return __ldg(row_scale + tc.row0 + r);
+  const int t = __ldg(token_of_row + tc.row0 + r);          // a bad one was recorded by the producer
+  return __ldg(row_scale + ((unsigned)t < (unsigned)n_tokens ? t : 0));
+}
+
 // One tile's epilogue for one warp: features col0 .. col0+31 (its TMEM lanes) of the tile's
 // tokens, 32 tokens per tcgen05.ld.  wscale multiplies every accumulator (the 4-bit
 // weights' per-tensor scale; 1 for bf16 weights).
@@ -126,11 +138,16 @@ __device__ __forceinline__ float wm_gate(const float* __restrict__ gate_of_row, 
 //   MODE 1: y[token][n] = gate_of_row[token] * wscale * acc.
 // g0, g1 (MODE 1): this lane's gates of the tile's first two 32-token chunks, fetched by the
 // caller before the accumulator was ready; later gates are fetched one chunk pair ahead.
-template <int MODE, typename OutT>
+// I8 (int32 accumulators): wscale and uscale are this lane's feature's weight scales (MODE 0:
+// gate and up; MODE 1: wscale alone), and the rows' scales come from row_scale.
+template <int MODE, typename OutT, bool I8 = false>
 __device__ __forceinline__ void wm_epilogue_tile(uint32_t taddr, uint8_t* stage, int lane, const TileCoord& tc,
                                                  int rank, int q, int d, int F, float wscale,
                                                  const float* __restrict__ gate_of_row, OutT* __restrict__ out,
-                                                 float g0 = 1.f, float g1 = 1.f) {
+                                                 float g0 = 1.f, float g1 = 1.f, float uscale = 1.f,
+                                                 const float* __restrict__ row_scale = nullptr,
+                                                 const int32_t* __restrict__ token_of_row = nullptr,
+                                                 int n_tokens = 0) {
   const int col0 = tc.n_tile * 256 + rank * kWRows + q * 32;   // this warp's first feature
   const int chunks = (tc.rows + 31) / 32;
   if constexpr (MODE == 0) {
@@ -138,6 +155,7 @@ __device__ __forceinline__ void wm_epilogue_tile(uint32_t taddr, uint8_t* stage,
     for (int c = 0; c < chunks; ++c) {
       const long long r0 = (long long)tc.row0 + c * 32;
       const int rv = min(32, tc.rows - c * 32);
+      const float sr = I8 ? wm_row_scale(row_scale, token_of_row, n_tokens, tc, c, lane) : 1.f;
       float h[32];
       uint32_t g[32], u[32];
       tmem_ld32(taddr + c * 32, g);
@@ -147,18 +165,34 @@ __device__ __forceinline__ void wm_epilogue_tile(uint32_t taddr, uint8_t* stage,
       tmem_regs_ready(u);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float gi = __uint_as_float(g[i]) * wscale;
+        float gi, ui;
+        if constexpr (I8) {
+          const float si = __shfl_sync(0xffffffffu, sr, i);
+          gi = acc_value<true>(g[i]) * (si * wscale);
+          ui = acc_value<true>(u[i]) * (si * uscale);
+        } else {
+          gi = __uint_as_float(g[i]) * wscale;
+          ui = __uint_as_float(u[i]) * wscale;
+        }
         // fast exp / divide: H is rounded to bf16 next, far coarser than their error
-        h[i] = __fdividef(gi, 1.f + __expf(-gi)) * (__uint_as_float(u[i]) * wscale);
+        h[i] = __fdividef(gi, 1.f + __expf(-gi)) * ui;
       }
       stage_store32_t<OutT>(stage, h, lane, out, r0, rv, F, col0, F);
     }
   } else {
     // two 32-token chunks per TMEM wait (the tile's mainloop is only K / 64 k-blocks)
     float ga = g0, gb = g1;
+    if (I8) {
+      ga *= wm_row_scale(row_scale, nullptr, 0, tc, 0, lane);
+      gb *= wm_row_scale(row_scale, nullptr, 0, tc, 1, lane);
+    }
 #pragma unroll 1
     for (int c = 0; c < chunks; c += 2) {
-      const float na = wm_gate(gate_of_row, tc, c + 2, lane), nb = wm_gate(gate_of_row, tc, c + 3, lane);
+      float na = wm_gate(gate_of_row, tc, c + 2, lane), nb = wm_gate(gate_of_row, tc, c + 3, lane);
+      if (I8) {
+        na *= wm_row_scale(row_scale, nullptr, 0, tc, c + 2, lane);
+        nb *= wm_row_scale(row_scale, nullptr, 0, tc, c + 3, lane);
+      }
       const bool two = c + 1 < chunks;                     // warp-uniform
       uint32_t v[32], vb[32];
       tmem_ld32(taddr + c * 32, v);
@@ -167,15 +201,23 @@ __device__ __forceinline__ void wm_epilogue_tile(uint32_t taddr, uint8_t* stage,
       tmem_regs_ready(v);
       tmem_regs_ready(vb);
       float h[32];
-      const float gs = ga * wscale;
+      const float gs = I8 ? ga : ga * wscale;              // I8: wscale is this lane's, not the row's
 #pragma unroll
-      for (int i = 0; i < 32; ++i) h[i] = __uint_as_float(v[i]) * __shfl_sync(0xffffffffu, gs, i);
+      for (int i = 0; i < 32; ++i) h[i] = acc_value<I8>(v[i]) * __shfl_sync(0xffffffffu, gs, i);
+      if (I8) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) h[i] *= wscale;
+      }
       stage_store32_t<OutT>(stage, h, lane, out, (long long)tc.row0 + c * 32, min(32, tc.rows - c * 32), d, col0,
                             d);
       if (two) {
-        const float gsb = gb * wscale;
+        const float gsb = I8 ? gb : gb * wscale;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) h[i] = __uint_as_float(vb[i]) * __shfl_sync(0xffffffffu, gsb, i);
+        for (int i = 0; i < 32; ++i) h[i] = acc_value<I8>(vb[i]) * __shfl_sync(0xffffffffu, gsb, i);
+        if (I8) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) h[i] *= wscale;
+        }
         stage_store32_t<OutT>(stage, h, lane, out, (long long)tc.row0 + (c + 1) * 32,
                               min(32, tc.rows - (c + 1) * 32), d, col0, d);
       }
@@ -189,12 +231,15 @@ __device__ __forceinline__ void wm_epilogue_tile(uint32_t taddr, uint8_t* stage,
 // token_of_row (no permuted copy of x): TMA row gathers (four rows per instruction, one
 // lane per four rows) land them in the same swizzled layout as the tiled loads, counted
 // on the even CTA's `full` barrier with the weights' bytes; tmX maps x with a one-row box.
-template <int MODE, typename OutT, bool GATHER = false>
+// I8: 8-bit rows and weights, read as rows of K two-byte elements (K = bytes / 2); row_scale by
+// row (GATHER: by token), w_scale [E][2F] or [E][d].
+template <int MODE, typename OutT, bool GATHER = false, bool I8 = false>
 __global__ void __launch_bounds__(WmCfg<MODE>::threads, 1)
 grouped_gemm_wm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                        const int32_t* __restrict__ offsets, int E, int K, int d, int F, long long rows_max,
                        const float* __restrict__ gate_of_row, OutT* __restrict__ out, int* err,
-                       const int32_t* __restrict__ token_of_row = nullptr, int n_tokens = 0) {
+                       const int32_t* __restrict__ token_of_row = nullptr, int n_tokens = 0,
+                       const float* __restrict__ row_scale = nullptr, const float* __restrict__ w_scale = nullptr) {
   static_assert(!GATHER || MODE == 0, "the gathered form is the gate/up GEMM's");
   using C = WmCfg<MODE>;
   extern __shared__ uint8_t smem_raw[];
@@ -341,7 +386,7 @@ grouped_gemm_wm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_con
         const int acc = it & 1;
         const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
         const TileCoord tc = tile_coord(tile_start, offsets, E, C::NT, tile);
-        const uint32_t idesc = make_idesc(2 * kWRows, wm_n<MODE>(tc.rows));
+        const uint32_t idesc = make_idesc_of<I8>(2 * kWRows, wm_n<MODE>(tc.rows));
         if (!mbar_wait(bar_tempty + 8 * acc, acc_phase ^ 1u, abort_flag, err)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * 256);
@@ -354,8 +399,8 @@ grouped_gemm_wm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_con
 #pragma unroll
           for (int kk = 0; kk < BK / UMMA_K; ++kk) {   // +32 bytes along K per step (>> 4 = 2)
             const uint32_t accumulate = (kb | kk) != 0 ? 1u : 0u;
-            umma_bf16_pair(d_tmem, adesc0 + 2 * kk, bdesc + 2 * kk, idesc, accumulate);
-            if (MODE == 0) umma_bf16_pair(d_tmem + 128, adesc1 + 2 * kk, bdesc + 2 * kk, idesc, accumulate);
+            umma_pair<I8>(d_tmem, adesc0 + 2 * kk, bdesc + 2 * kk, idesc, accumulate);
+            if (MODE == 0) umma_pair<I8>(d_tmem + 128, adesc1 + 2 * kk, bdesc + 2 * kk, idesc, accumulate);
           }
           umma_commit_pair_both(bar_empty + 8 * stage);
           if (++stage == C::stages) { stage = 0; phase ^= 1u; }
@@ -378,12 +423,20 @@ grouped_gemm_wm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_con
       // the first gates, fetched while the tile's MMAs still run
       const float g0 = MODE == 1 ? wm_gate(gate_of_row, tc, 0, lane) : 1.f;
       const float g1 = MODE == 1 ? wm_gate(gate_of_row, tc, 1, lane) : 1.f;
+      float sw = 1.f, su = 1.f;
+      if (I8) {                                              // this lane's feature's weight scales
+        const int f = tc.n_tile * 256 + (int)rank * kWRows + q * 32 + lane, n = MODE == 0 ? F : d;
+        const float* p = w_scale + (long long)tc.e * (MODE == 0 ? 2 * F : d);
+        sw = f < n ? __ldg(p + f) : 0.f;
+        su = MODE == 0 && f < n ? __ldg(p + F + f) : 0.f;
+      }
       const bool got = mbar_wait(bar_tfull + 8 * acc, acc_phase, abort_flag, err);
       if (!__all_sync(0xffffffffu, got)) break;
       __syncwarp();
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
-      wm_epilogue_tile<MODE, OutT>(taddr, stage, lane, tc, (int)rank, q, d, F, 1.f, gate_of_row, out, g0, g1);
+      wm_epilogue_tile<MODE, OutT, I8>(taddr, stage, lane, tc, (int)rank, q, d, F, sw, gate_of_row, out, g0, g1, su,
+                                       row_scale, GATHER ? token_of_row : nullptr, n_tokens);
       tc_fence_before();
       mbar_arrive_remote(map_to_rank(bar_tempty + 8 * acc, 0));
     }
@@ -776,13 +829,14 @@ fp4_scales_kernel(const uint8_t* __restrict__ in, long long rows, int K, int spr
   }
 }
 
-template <int MODE, typename OutT, bool GATHER = false>
+template <int MODE, typename OutT, bool GATHER = false, bool I8 = false>
 moe_status launch_wm(const CUtensorMap& mw, const CUtensorMap& mx, const int32_t* offsets, int E, int K, int d,
                      int F, long long rows_max, const float* gate_of_row, void* out, cudaStream_t s,
-                     const int32_t* token_of_row = nullptr, int n_tokens = 0) {
+                     const int32_t* token_of_row = nullptr, int n_tokens = 0, const float* row_scale = nullptr,
+                     const float* w_scale = nullptr) {
   using C = WmCfg<MODE>;
   static std::atomic<int> configured[kMaxDevices];
-  const moe_status st = ensure_smem_limit(configured, grouped_gemm_wm_kernel<MODE, OutT, GATHER>, C::smem);
+  const moe_status st = ensure_smem_limit(configured, grouped_gemm_wm_kernel<MODE, OutT, GATHER, I8>, C::smem);
   if (st != MOE_OK) return st;
   const long long max_tiles = ((rows_max + C::NT - 1) / C::NT + E) * (long long)wm_m_tiles<MODE>(F, d);
   int pairs = num_sms() / 2;
@@ -800,9 +854,9 @@ moe_status launch_wm(const CUtensorMap& mw, const CUtensorMap& mx, const int32_t
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, grouped_gemm_wm_kernel<MODE, OutT, GATHER>, mw, mx, offsets, E, K, d,
-                                        F, rows_max, gate_of_row, static_cast<OutT*>(out), err_ptr(), token_of_row,
-                                        n_tokens));
+  return cuda_status(cudaLaunchKernelEx(&cfg, grouped_gemm_wm_kernel<MODE, OutT, GATHER, I8>, mw, mx, offsets, E, K,
+                                        d, F, rows_max, gate_of_row, static_cast<OutT*>(out), err_ptr(), token_of_row,
+                                        n_tokens, row_scale, w_scale));
 }
 
 }  // namespace
@@ -858,6 +912,39 @@ moe_status launch_down_wm(const void* h, const int32_t* offsets, int E, int d, i
   if (!make_map(&mx, h, (unsigned long long)rows_max, F, kWXBox)) return MOE_ERR_UNSUPPORTED;
   if (y_dtype == MOE_F32) return launch_wm<1, float>(mw, mx, offsets, E, F, d, F, rows_max, gate_of_row, y_rows, s);
   return launch_wm<1, __nv_bfloat16>(mw, mx, offsets, E, F, d, F, rows_max, gate_of_row, y_rows, s);
+}
+
+// 8-bit rows and weights, weight-major: the same tiles over rows of K / 2 two-byte elements.
+moe_status launch_gate_up_wm_i8(const int8_t* x_q, const float* x_scale, const int32_t* offsets, int E, int d, int F,
+                                long long rows_max, const int8_t* W, const float* w_scale, void* h, cudaStream_t s) {
+  CUtensorMap mw, mx;
+  if (!make_map(&mw, W, (unsigned long long)E * 2 * F, d / 2, kWRows)) return MOE_ERR_UNSUPPORTED;
+  if (!make_map(&mx, x_q, (unsigned long long)rows_max, d / 2, kWXBox)) return MOE_ERR_UNSUPPORTED;
+  return launch_wm<0, __nv_bfloat16, false, true>(mw, mx, offsets, E, d / 2, d, F, rows_max, nullptr, h, s, nullptr, 0,
+                                                  x_scale, w_scale);
+}
+
+moe_status launch_gate_up_gather_i8(const int8_t* x_q, const float* x_scale, const int32_t* token_of_row, int T,
+                                    const int32_t* offsets, int E, int d, int F, long long rows_max, const int8_t* W,
+                                    const float* w_scale, void* h, cudaStream_t s) {
+  CUtensorMap mw, mx;
+  if (!make_map(&mw, W, (unsigned long long)E * 2 * F, d / 2, kWRows)) return MOE_ERR_UNSUPPORTED;
+  if (!make_map(&mx, x_q, (unsigned long long)T, d / 2, 1)) return MOE_ERR_UNSUPPORTED;   // row gathers
+  return launch_wm<0, __nv_bfloat16, true, true>(mw, mx, offsets, E, d / 2, d, F, rows_max, nullptr, h, s,
+                                                 token_of_row, T, x_scale, w_scale);
+}
+
+moe_status launch_down_wm_i8(const int8_t* h_q, const float* h_scale, const int32_t* offsets, int E, int d, int F,
+                             long long rows_max, const int8_t* W, const float* w_scale, const float* gate_of_row,
+                             int y_dtype, void* y_rows, cudaStream_t s) {
+  CUtensorMap mw, mx;
+  if (!make_map(&mw, W, (unsigned long long)E * d, F / 2, kWRows)) return MOE_ERR_UNSUPPORTED;
+  if (!make_map(&mx, h_q, (unsigned long long)rows_max, F / 2, kWXBox)) return MOE_ERR_UNSUPPORTED;
+  if (y_dtype == MOE_F32)
+    return launch_wm<1, float, false, true>(mw, mx, offsets, E, F / 2, d, F, rows_max, gate_of_row, y_rows, s, nullptr,
+                                            0, h_scale, w_scale);
+  return launch_wm<1, __nv_bfloat16, false, true>(mw, mx, offsets, E, F / 2, d, F, rows_max, gate_of_row, y_rows, s,
+                                                  nullptr, 0, h_scale, w_scale);
 }
 
 // Gate/up and down with 4-bit weights, weight-major.  Codes [rows, K/2] as

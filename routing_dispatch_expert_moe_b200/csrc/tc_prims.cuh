@@ -20,6 +20,14 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s per barrier 
 constexpr uint32_t make_idesc(int m, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+// instruction descriptor of kind::i8: D int32, A and B signed 8-bit, both K-major
+constexpr uint32_t make_idesc_i8(int m, int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+template <bool I8>
+constexpr uint32_t make_idesc_of(int m, int n) {
+  return I8 ? make_idesc_i8(m, n) : make_idesc(m, n);
+}
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -174,6 +182,42 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t adesc, 
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// kind::i8: 32 signed bytes along K per MMA, the same 32 bytes that 16 bf16 take, so the operand
+// blocks, descriptors and k steps are those of the bf16 MMAs with a row read as K / 2 bf16.
+__device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+template <bool I8>
+__device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  if constexpr (I8) umma_i8(d_tmem, adesc, bdesc, idesc, acc);
+  else umma_bf16(d_tmem, adesc, bdesc, idesc, acc);
+}
+template <bool I8>
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t acc) {
+  if constexpr (I8) umma_i8_pair(d_tmem, adesc, bdesc, idesc, acc);
+  else umma_bf16_pair(d_tmem, adesc, bdesc, idesc, acc);
+}
+// An accumulator register as a number: fp32 bits, or an int32 (at most 2^28: rounded to fp32).
+template <bool I8>
+__device__ __forceinline__ float acc_value(uint32_t r) {
+  return I8 ? __int2float_rn((int)r) : __uint_as_float(r);
 }
 // Completion of the pair's MMAs arrives on the barrier at this offset in both CTAs.
 __device__ __forceinline__ void umma_commit_pair_both(uint32_t bar) {

@@ -20,6 +20,7 @@ LIB_PATH = os.environ.get("MOE_B200_LIB", os.path.join(_HERE, "libmoe_b200.so"))
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE = range(6)
 SCORE = {"softmax": 0, "sigmoid": 1, "sqrt_softplus": 2}
 SELECT = {"uniform": 0, "hash": 1}
+GROUP_SCORE = {"max": 0, "top2": 1}
 FP4 = {"mxfp4": 0, "nvfp4": 1}
 DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 DEVERR = {0: "none", 1: "expert id out of range", 2: "duplicate expert in a token", 3: "row index out of range",
@@ -94,6 +95,27 @@ _SIGNATURES = {
     "moe_round_output": (_i32, [_c_void_p, _i64, _c_void_p, _i32, _c_void_p]),
     "moe_fp4_scales_bytes": (_size, [_i64, _i32, _i32]),
     "moe_prepare_fp4_scales": (_i32, [_c_void_p, _i64, _i32, _i32, _c_void_p, _size, _c_void_p]),
+    "moe_route_grouped": (_i32, [_c_void_p, _c_void_p, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32,
+                                 _c_void_p, _c_void_p, _c_void_p]),
+    "moe_route_backward": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _i32, _i32, _i32, _i32, _f32, _c_void_p,
+                                  _f32, _f32, _c_void_p, _c_void_p]),
+    "moe_quantize_rows_i8": (_i32, [_c_void_p, _i32, _i64, _i32, _c_void_p, _i32, _i64, _c_void_p, _c_void_p,
+                                    _c_void_p]),
+    "moe_expert_gate_up_i8": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _i32, _i32, _i64, _c_void_p, _c_void_p,
+                                     _c_void_p, _c_void_p]),
+    "moe_expert_gate_up_gather_i8": (_i32, [_c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p, _i32, _i32, _i32, _i64,
+                                            _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_expert_down_i8": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _i32, _i32, _i64, _c_void_p, _c_void_p,
+                                  _c_void_p, _i32, _c_void_p, _c_void_p]),
+    "moe_block_norm": (_i32, [_c_void_p, _i32, _c_void_p, _i32, _c_void_p, _c_void_p, _i32, _f32, _c_void_p, _f32,
+                              _i32, _i32, _c_void_p, _c_void_p, _i32, _c_void_p]),
+    "moe_combine_norm": (_i32, [_c_void_p, _i32, _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _i32, _i64,
+                                _c_void_p, _c_void_p, _i32, _f32, _c_void_p, _f32, _i32, _i32, _c_void_p, _c_void_p,
+                                _c_void_p, _i32, _c_void_p]),
+    "moe_block_norm_backward_workspace_bytes": (_size, [_i32, _i32, _i32]),
+    "moe_block_norm_backward": (_i32, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32, _i32, _i32, _c_void_p,
+                                       _c_void_p, _i32, _f32, _c_void_p, _f32, _i32, _i32, _c_void_p, _c_void_p,
+                                       _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p]),
     "moe_expert_gate_up_fp4": (_i32, [_c_void_p, _c_void_p, _i32, _i32, _i32, _i64, _c_void_p, _c_void_p, _i32,
                                       _c_void_p, _c_void_p, _c_void_p]),
     "moe_expert_down_fp4": (_i32, [_c_void_p, _c_void_p, _i32, _i32, _i32, _i64, _c_void_p, _c_void_p, _i32,
@@ -655,6 +677,289 @@ def moe_router_stats(logits, counts, kept, k: int, score: str = "softmax", load=
     _check("moe_router_stats", lib().moe_router_stats(_p(logits), _p(counts), _p(kept), T, E, k, SCORE[score],
                                                       _p(load), _p(stats5), _p(ws), nb, _stream(stream)))
     return load, stats5
+
+
+# ---------------------------------------------------------------- groups, 8-bit experts, block norms
+class _on:
+    """Makes the device of `t` current for a call, and checks that the other tensors are on it."""
+
+    __slots__ = ("index", "back")
+
+    def __init__(self, t: torch.Tensor, *others):
+        self.index = t.get_device()
+        for o in others:
+            if o is not None and o.get_device() != self.index:
+                raise ValueError(f"every tensor of a call must be on one device: {o.device} beside {t.device}")
+
+    def __enter__(self):
+        self.back = torch.cuda.current_device()
+        if self.back != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.back != self.index:
+            torch.cuda.set_device(self.back)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _cuda_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _rows_of(t: torch.Tensor, name: str, rows: int, cols=None, dtype=None):
+    """A contiguous buffer of at least `rows` rows (of `cols` elements, when it has two dimensions)."""
+    _need(t, name, dtype)
+    if t.dim() != (1 if cols is None else 2) or t.shape[0] < rows or (cols is not None and t.shape[1] != cols):
+        want = f"({rows},)" if cols is None else f"({rows}, {cols})"
+        raise ValueError(f"{name} must have at least {want} entries, got {tuple(t.shape)}")
+    return t
+
+
+def _choice(table: dict, key: str, name: str) -> int:
+    if key not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {key!r}")
+    return table[key]
+
+
+def moe_route_grouped(logits, k: int, n_groups: int, groups_kept: int, group_score: str = "top2",
+                      score: str = "sigmoid", renormalize: bool = True, scale: float = 1.0, select_bias=None,
+                      topk_idx=None, topk_gate=None, stream=None):
+    """Top-k of logits [T, E] within the groups_kept best of n_groups groups of neighbouring
+    experts.  A -inf or NaN logit masks its expert.  Returns (topk_idx [T,k] i32, topk_gate [T,k] f32)."""
+    _need(logits, "logits", torch.float32)
+    T, E = logits.shape
+    if select_bias is not None:
+        _need(select_bias, "select_bias", torch.float32, (E,))
+    dev = logits.device
+    topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_idx is None else \
+        _need(topk_idx, "topk_idx", torch.int32, (T, k))
+    topk_gate = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_gate is None else \
+        _need(topk_gate, "topk_gate", torch.float32, (T, k))
+    with _on(logits, select_bias, topk_idx, topk_gate):
+        _check("moe_route_grouped", lib().moe_route_grouped(
+            _ptr(logits), _ptr(select_bias), T, E, k, n_groups, groups_kept,
+            _choice(GROUP_SCORE, group_score, "group_score"), _choice(SCORE, score, "score"), 1 if renormalize else 0,
+            scale, _ptr(topk_idx), _ptr(topk_gate), _cuda_stream(stream)))
+    return topk_idx, topk_gate
+
+
+def moe_route_backward(logits, topk_idx=None, d_gate=None, score: str = "softmax", renormalize: bool = True,
+                       scale: float = 1.0, load=None, aux_coef: float = 0.0, z_coef: float = 0.0, d_logits=None,
+                       stream=None):
+    """Gradient by the logits [T, E] of the gates (d_gate [T, k] of topk_idx [T, k]) plus
+    aux_coef times that of the load-balancing loss (load: moe_router_stats' f_e) and z_coef times
+    that of the z-loss.  Returns d_logits [T, E] f32."""
+    _need(logits, "logits", torch.float32)
+    T, E = logits.shape
+    k = 0
+    if topk_idx is not None:
+        _need(topk_idx, "topk_idx", torch.int32)
+        k = topk_idx.shape[1] if topk_idx.dim() == 2 else 0
+        _need(topk_idx, "topk_idx", None, (T, k))
+    if d_gate is not None:
+        _need(d_gate, "d_gate", torch.float32, (T, k))
+    if load is not None:
+        _need(load, "load", torch.float32, (E,))
+    d_logits = torch.empty_like(logits) if d_logits is None else _need(d_logits, "d_logits", torch.float32, (T, E))
+    with _on(logits, topk_idx, d_gate, load, d_logits):
+        _check("moe_route_backward", lib().moe_route_backward(
+            _ptr(logits), _ptr(topk_idx), _ptr(d_gate), T, E, k, _choice(SCORE, score, "score"),
+            1 if renormalize else 0, scale, _ptr(load), aux_coef, z_coef, _ptr(d_logits), _cuda_stream(stream)))
+    return d_logits
+
+
+def moe_quantize_rows_i8(x, row_of=None, rows_max: int = 0, q=None, scale=None, stream=None):
+    """Rows of x [rows, cols] (bf16 or fp32) to 8-bit integers with a scale each.  With row_of
+    [rows, k] the dispatch is fused into it: token t's bytes and scale go to rows row_of[t] of q
+    [rows_max, cols] (rows nothing is sent to are left as they are).  Returns (q int8, scale f32)."""
+    _need(x, "x")
+    rows, cols = x.shape
+    k, out = 1, rows
+    if row_of is not None:
+        _need(row_of, "row_of", torch.int32)
+        k, out = row_of.shape[1], rows_max
+        _need(row_of, "row_of", None, (rows, k))
+    q = torch.empty((out, cols), dtype=torch.int8, device=x.device) if q is None else \
+        _rows_of(q, "q", out, cols, torch.int8)
+    scale = torch.empty((out,), dtype=torch.float32, device=x.device) if scale is None else \
+        _rows_of(scale, "scale", out, None, torch.float32)
+    with _on(x, row_of, q, scale):
+        _check("moe_quantize_rows_i8", lib().moe_quantize_rows_i8(
+            _ptr(x), _dt(x), rows, cols, _ptr(row_of), k, out, _ptr(q), _ptr(scale), _cuda_stream(stream)))
+    return q, scale
+
+
+def quantize_experts_i8(W, stream=None):
+    """Stacked expert weights W [E, N, K] (bf16 or fp32, on the device) to 8 bits with a scale for
+    each output channel, once at load time.  Returns (q int8 [E, N, K], scale f32 [E, N])."""
+    E, N, K = W.shape
+    q, scale = moe_quantize_rows_i8(W.reshape(E * N, K), stream=stream)
+    return q.view(E, N, K), scale.view(E, N)
+
+
+def moe_expert_gate_up_i8(x_q, x_scale, offsets, W_gu, w_scale, rows_max: int, h=None, token_of_row=None,
+                          stream=None):
+    """H = silu(X Wg^T) * (X Wu^T) in bf16 from 8-bit rows x_q [rows_max, d] with x_scale [rows_max]
+    and weights W_gu [E, 2F, d] int8 with w_scale [E, 2F].  With token_of_row the rows are read
+    from x_q [T, d], x_scale [T] instead (moe_expert_gate_up_gather_i8)."""
+    _need(W_gu, "W_gu", torch.int8)
+    E, F2, d = W_gu.shape
+    F = F2 // 2
+    _need(w_scale, "w_scale", torch.float32, (E, F2))
+    _need(offsets, "offsets", torch.int32, (E + 1,))
+    T = x_q.shape[0]
+    rows = rows_max if token_of_row is None else T
+    _rows_of(x_q, "x_q", rows, d, torch.int8)
+    _rows_of(x_scale, "x_scale", rows, None, torch.float32)
+    h = torch.empty((rows_max, F), dtype=torch.bfloat16, device=x_q.device) if h is None else \
+        _rows_of(h, "h", rows_max, F, torch.bfloat16)
+    with _on(x_q, x_scale, offsets, W_gu, w_scale, h, token_of_row):
+        if token_of_row is None:
+            _check("moe_expert_gate_up_i8", lib().moe_expert_gate_up_i8(
+                _ptr(x_q), _ptr(x_scale), _ptr(offsets), E, d, F, rows_max, _ptr(W_gu), _ptr(w_scale), _ptr(h),
+                _cuda_stream(stream)))
+        else:
+            _rows_of(token_of_row, "token_of_row", rows_max, None, torch.int32)
+            _check("moe_expert_gate_up_gather_i8", lib().moe_expert_gate_up_gather_i8(
+                _ptr(x_q), _ptr(x_scale), T, _ptr(token_of_row), _ptr(offsets), E, d, F, rows_max, _ptr(W_gu),
+                _ptr(w_scale), _ptr(h), _cuda_stream(stream)))
+    return h
+
+
+def moe_expert_down_i8(h_q, h_scale, offsets, W_dn, w_scale, rows_max: int, gate_of_row=None, y_rows=None,
+                       y_dtype=None, stream=None):
+    """Gated rows = gate_of_row * (H W_dn^T) from 8-bit rows h_q [rows_max, F] with h_scale and
+    weights W_dn [E, d, F] int8 with w_scale [E, d], in y_dtype (default: y_rows' dtype, else fp32)."""
+    _need(W_dn, "W_dn", torch.int8)
+    E, d, F = W_dn.shape
+    _need(w_scale, "w_scale", torch.float32, (E, d))
+    _need(offsets, "offsets", torch.int32, (E + 1,))
+    _rows_of(h_q, "h_q", rows_max, F, torch.int8)
+    _rows_of(h_scale, "h_scale", rows_max, None, torch.float32)
+    if gate_of_row is not None:
+        _rows_of(gate_of_row, "gate_of_row", rows_max, None, torch.float32)
+    y_rows = torch.empty((rows_max, d), dtype=y_dtype or torch.float32, device=h_q.device) if y_rows is None else \
+        _rows_of(y_rows, "y_rows", rows_max, d, y_dtype)
+    with _on(h_q, h_scale, offsets, W_dn, w_scale, gate_of_row, y_rows):
+        _check("moe_expert_down_i8", lib().moe_expert_down_i8(
+            _ptr(h_q), _ptr(h_scale), _ptr(offsets), E, d, F, rows_max, _ptr(W_dn), _ptr(w_scale), _ptr(gate_of_row),
+            _dt(y_rows), _ptr(y_rows), _cuda_stream(stream)))
+    return y_rows
+
+
+def _norm_params(d, post_weight, gate, pre_weight):
+    for t, n in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
+        if t is not None:
+            _need(t, n, torch.float32, (d,))
+    if gate is None:
+        return 1
+    _need(gate, "gate", torch.float32)
+    if gate.dim() != 2 or gate.shape[1] != d:
+        raise ValueError(f"gate must be [rows, {d}], got {tuple(gate.shape)}")
+    return gate.shape[0]
+
+
+def _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, want_x):
+    shape = residual.shape
+    if x_out is not None:
+        _need(x_out, "x_out", residual.dtype, shape)
+    elif want_x:
+        x_out = torch.empty_like(residual)
+    if n_out is not None:
+        _need(n_out, "n_out", n_dtype, shape)
+    elif pre_weight is not None:
+        n_out = torch.empty(shape, dtype=n_dtype or torch.bfloat16, device=residual.device)
+    return x_out, n_out
+
+
+def moe_block_norm(residual, y=None, post_weight=None, gate=None, alpha: float = 1.0, pre_weight=None,
+                   eps: float = 1e-6, x_out=None, n_out=None, n_dtype=None, stream=None):
+    """x' = alpha residual + gate * norm(y) post_weight, n = norm(x') pre_weight, on rows [T, d].
+    y None: x' = alpha residual, written only if x_out is given.  gate [G, d], G dividing T.
+    n_dtype defaults to n_out's, else bf16.  Returns (x_out or None, n_out or None)."""
+    _need(residual, "residual")
+    T, d = residual.shape
+    if y is not None:
+        _need(y, "y", None, (T, d))
+    G = _norm_params(d, post_weight, gate, pre_weight)
+    x_out, n_out = _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, y is not None)
+    rt = _dt(residual)
+    with _on(residual, y, post_weight, gate, pre_weight, x_out, n_out):
+        _check("moe_block_norm", lib().moe_block_norm(
+            _ptr(residual), rt, _ptr(y), rt if y is None else _dt(y), _ptr(post_weight), _ptr(gate), G, alpha,
+            _ptr(pre_weight), eps, T, d, _ptr(x_out), _ptr(n_out), rt if n_out is None else _dt(n_out),
+            _cuda_stream(stream)))
+    return x_out, n_out
+
+
+def moe_combine_norm(residual, y_rows, row_of, rows_max: int, topk_gate=None, shared_y=None, post_weight=None,
+                     gate=None, alpha: float = 1.0, pre_weight=None, eps: float = 1e-6, y_out=None, x_out=None,
+                     n_out=None, n_dtype=None, stream=None):
+    """moe_block_norm of moe_combine's sum (which y_out, if given, receives in y_rows' dtype).
+    Returns (x_out, n_out or None)."""
+    _need(residual, "residual")
+    T, d = residual.shape
+    _rows_of(y_rows, "y_rows", rows_max, d)
+    _need(row_of, "row_of", torch.int32)
+    k = row_of.shape[1] if row_of.dim() == 2 else 0
+    _need(row_of, "row_of", None, (T, k))
+    if topk_gate is not None:
+        _need(topk_gate, "topk_gate", torch.float32, (T, k))
+    for t, n in ((shared_y, "shared_y"), (y_out, "y_out")):
+        if t is not None:
+            _need(t, n, y_rows.dtype, (T, d))
+    G = _norm_params(d, post_weight, gate, pre_weight)
+    x_out, n_out = _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, True)
+    rt = _dt(residual)
+    with _on(residual, y_rows, row_of, topk_gate, shared_y, post_weight, gate, pre_weight, y_out, x_out, n_out):
+        _check("moe_combine_norm", lib().moe_combine_norm(
+            _ptr(residual), rt, _ptr(y_rows), _dt(y_rows), _ptr(row_of), _ptr(topk_gate), _ptr(shared_y), k, rows_max,
+            _ptr(post_weight), _ptr(gate), G, alpha, _ptr(pre_weight), eps, T, d, _ptr(y_out), _ptr(x_out),
+            _ptr(n_out), rt if n_out is None else _dt(n_out), _cuda_stream(stream)))
+    return x_out, n_out
+
+
+def moe_block_norm_backward(d_x, d_n, x_out, y=None, post_weight=None, gate=None, alpha: float = 1.0,
+                            pre_weight=None, eps: float = 1e-6, d_residual=None, d_y=None, d_post_weight=None,
+                            d_gate=None, d_pre_weight=None, workspace=None, stream=None):
+    """Gradients of moe_block_norm from its saved x_out [T, d] and y, for the gradients d_x of x_out
+    and d_n of n_out (either may be None; d_n goes with pre_weight).  Returns dict(d_residual, d_y,
+    d_post_weight, d_gate, d_pre_weight), None where the input is absent."""
+    _need(x_out, "x_out")
+    T, d = x_out.shape
+    dev = x_out.device
+    if d_x is not None:
+        _need(d_x, "d_x", x_out.dtype, (T, d))
+    for t, n in ((d_n, "d_n"), (y, "y")):
+        if t is not None:
+            _need(t, n, None, (T, d))
+    G = _norm_params(d, post_weight, gate, pre_weight)
+
+    def out(t, name, like, dtype):
+        if t is not None:
+            return _need(t, name, dtype, None if like is None else like.shape)
+        return None if like is None else torch.empty(like.shape, dtype=dtype, device=dev)
+
+    f32 = torch.float32
+    d_residual = out(d_residual, "d_residual", x_out, x_out.dtype)
+    d_y = out(d_y, "d_y", y, None if y is None else y.dtype)
+    d_post_weight = out(d_post_weight, "d_post_weight", post_weight, f32)
+    d_gate = out(d_gate, "d_gate", gate, f32)
+    d_pre_weight = out(d_pre_weight, "d_pre_weight", pre_weight, f32)
+    rt = _dt(x_out)
+    with _on(x_out, d_x, d_n, y, post_weight, gate, pre_weight, d_residual, d_y, d_post_weight, d_gate, d_pre_weight,
+             workspace):
+        nb = lib().moe_block_norm_backward_workspace_bytes(T, d, G)
+        ws = _ws(nb, dev, workspace)
+        _check("moe_block_norm_backward", lib().moe_block_norm_backward(
+            _ptr(d_x), _ptr(d_n), _ptr(x_out), _ptr(y), rt, rt if d_n is None else _dt(d_n), rt if y is None else _dt(y),
+            _ptr(post_weight), _ptr(gate), G, alpha, _ptr(pre_weight), eps, T, d, _ptr(d_residual), _ptr(d_y),
+            _ptr(d_post_weight), _ptr(d_gate), _ptr(d_pre_weight), _ptr(ws), nb, _cuda_stream(stream)))
+    return {"d_residual": d_residual, "d_y": d_y, "d_post_weight": d_post_weight, "d_gate": d_gate,
+            "d_pre_weight": d_pre_weight}
 
 
 def moe_get_device_error(stream=None) -> int:
