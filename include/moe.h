@@ -842,10 +842,10 @@ MOE_API moe_status moe_expert_down_i8(const int8_t* h_q, const float* h_scale, c
  *   d_residual  (device) [T, d] r_dtype out; may be d_x itself
  *   d_y         (device) [T, d] y_dtype out; required with y
  *   d_post_weight [d], d_gate [gate_rows, d], d_pre_weight [d] (device) fp32 out, each NULL or
- *               its input given.  Column sums are fp32 per block of tokens, then fp64 in a fixed
- *               order: results repeat bit for bit.
- *   workspace   (device) >= moe_block_norm_backward_workspace_bytes(T, d, gate_rows), gate_rows
- *               1 without a gate; calls that overlap need one each
+ *               its input given.  Column sums are fp32 per block of tokens, then over the blocks
+ *               in a fixed order: results repeat bit for bit.
+ *   workspace   (device) >= moe_block_norm_backward_workspace_bytes(T, d) bytes (of the current
+ *               device); calls that overlap need one each
  * T = 0 clears the weight gradients.
  * Errors: as above; INVALID_ARG also when a gradient is asked for without its input, or neither
  * d_x nor d_n is given; WORKSPACE if too small.
@@ -860,7 +860,7 @@ MOE_API moe_status moe_combine_norm(const void* residual, int32_t r_dtype, const
                      const float* gate, int32_t gate_rows, float alpha, const float* pre_weight,
                      float eps, int32_t T, int32_t d, void* y_out, void* x_out, void* n_out,
                      int32_t n_dtype, void* stream);
-MOE_API size_t moe_block_norm_backward_workspace_bytes(int32_t T, int32_t d, int32_t gate_rows);
+MOE_API size_t moe_block_norm_backward_workspace_bytes(int32_t T, int32_t d);
 MOE_API moe_status moe_block_norm_backward(const void* d_x, const void* d_n, const void* x_out, const void* y,
                      int32_t r_dtype, int32_t n_dtype, int32_t y_dtype, const float* post_weight,
                      const float* gate, int32_t gate_rows, float alpha, const float* pre_weight,

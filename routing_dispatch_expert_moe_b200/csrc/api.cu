@@ -702,9 +702,9 @@ moe_status moe_combine_norm(const void* residual, int32_t r_dtype, const void* y
                            S(stream));
 }
 
-size_t moe_block_norm_backward_workspace_bytes(int32_t T, int32_t d, int32_t gate_rows) {
-  if (T < 1 || d < 1 || gate_rows < 1 || T % gate_rows != 0) return 0;
-  return block_norm_grad_workspace_bytes(T, d, gate_rows);
+size_t moe_block_norm_backward_workspace_bytes(int32_t T, int32_t d) {
+  if (T < 1 || d < 1) return 0;
+  return block_norm_grad_workspace_bytes(T, d);
 }
 
 moe_status moe_block_norm_backward(const void* d_x, const void* d_n, const void* x_out, const void* y, int32_t r_dtype,
@@ -730,7 +730,7 @@ moe_status moe_block_norm_backward(const void* d_x, const void* d_n, const void*
       !aligned16(gate) || !aligned16(pre_weight) || !aligned16(d_residual) || !aligned16(d_y) || !aligned16(d_gate) ||
       !aligned16(workspace))
     return MOE_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < block_norm_grad_workspace_bytes(T, d, gate_rows)) return MOE_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < block_norm_grad_workspace_bytes(T, d)) return MOE_ERR_WORKSPACE;
   return launch_block_norm_backward(d_x, d_n, x_out, y, y_dtype, r_dtype, n_dtype, post_weight, gate, gate_rows, alpha,
                                     pre_weight, eps, T, d, d_residual, d_y, d_post_weight, d_gate, d_pre_weight,
                                     workspace, S(stream));

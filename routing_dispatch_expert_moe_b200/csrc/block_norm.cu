@@ -17,11 +17,13 @@
 // Bound by HBM: each input is read once and each output written once, the row between them in
 // registers.  A block of TPR threads has a row; a thread has V vectors of eight neighbouring
 // elements.  Sums are fp32: a thread's elements, a shuffle, then the warps' sums through shared
-// memory.  The backward pass gives each block a run of rows of one gate group; it keeps the
-// weights' column sums in registers over all its rows and writes them out once, and a second
-// kernel adds the blocks' partial sums in a fixed order in fp64 (results repeat bit for bit).
+// memory.  The backward pass gives each block runs of rows, each of one gate group; it keeps the
+// column sums in registers over a run (the gate's and the post-norm weight's are one sum,
+// sum_t u yh, times the other's value) and over all its rows (the pre-norm weight's), and a
+// second kernel adds the blocks' partial sums in a fixed order (results repeat bit for bit).
 #include "common.cuh"
-#include "row8.cuh"
+#include "f32x2.cuh"
+#include "tc_prims.cuh"
 
 namespace moe {
 namespace {
@@ -29,8 +31,20 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kNormMaxWarps = 16;
 
-// Sum of two values over the block; `part` is this call's own slice of shared
-// memory, so that a row needs one barrier for each reduction.
+// Sums over the block; `part` is this call's own slice of shared memory, so that a row needs one
+// barrier for each reduction.  Every warp adds the warps' sums itself (at most 16: four steps).
+__device__ __forceinline__ float block_sum(float a, float* part, int warps) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(kFull, a, o);
+  if (warps == 1) return a;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) part[threadIdx.x >> 5] = a;
+  __syncthreads();
+  a = (lane & 15) < warps ? part[lane & 15] : 0.f;
+#pragma unroll
+  for (int o = 8; o; o >>= 1) a += __shfl_xor_sync(kFull, a, o);
+  return a;
+}
 __device__ __forceinline__ float2 block_sum2(float a, float b, float2* part, int warps) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
@@ -38,31 +52,46 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float2* part, int
     b += __shfl_xor_sync(kFull, b, o);
   }
   if (warps == 1) return make_float2(a, b);
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  if (lane == 0) part[w] = make_float2(a, b);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) part[threadIdx.x >> 5] = make_float2(a, b);
   __syncthreads();
-  float2 s = lane < warps ? part[lane] : make_float2(0.f, 0.f);
+  float2 s = (lane & 15) < warps ? part[lane & 15] : make_float2(0.f, 0.f);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
+  for (int o = 8; o; o >>= 1) {
     s.x += __shfl_xor_sync(kFull, s.x, o);
     s.y += __shfl_xor_sync(kFull, s.y, o);
   }
   return s;
 }
+// 1 / rms from a row's sum of squares (rsqrtf: within 2 steps).
+__device__ __forceinline__ float inv_rms(float ss, float inv_d, float eps) { return rsqrtf(fmaf(ss, inv_d, eps)); }
 
+// Eight elements of a row in its storage type, as loaded; `oct` makes them pairs of fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const void* base, long long e, float* f) {
-  Row8<T> r;
-  r.load(base, e);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = 0.f;
-  r.add(f, 1.f, false);
-}
-__device__ __forceinline__ void param8(const float* p, long long e, float* f) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p + e));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p + e + 4));
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const void* base, long long e) {
+    a = ld_stream(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + e));
+  }
+  __device__ __forceinline__ Oct oct() const { return oct_bf16(a); }
+};
+template <>
+struct Raw8<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const void* base, long long e) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + e);
+    a = ld_stream(p);
+    b = ld_stream(p + 1);
+  }
+  __device__ __forceinline__ Oct oct() const { return oct_f32(a, b); }
+};
+// Eight of a parameter's values, or ones where it is not given.
+__device__ __forceinline__ Oct param8(const float* p, long long e) {
+  if (!p) return oct_const(1.f);
+  const uint4* q = reinterpret_cast<const uint4*>(p + e);
+  return oct_f32(__ldg(q), __ldg(q + 1));
 }
 
 struct NormArgs {
@@ -78,120 +107,120 @@ struct NormArgs {
   void* x_out;                // [T, d] or null
   void* n_out;                // [T, d] or null
   long long rows_max;
-  float alpha, eps;
+  float alpha, eps, inv_d;    // inv_d = 1 / d
   int T, d, per_gate, k;      // per_gate: tokens that share a gate row
   int* err;
 };
 
 // YT: y or the expert rows; RT: the residual stream; NT: the normed rows.
 template <typename YT, typename RT, typename NT, int V, bool COMBINE>
-__global__ void __launch_bounds__(V == 1 ? 256 : 512)
+__global__ void __launch_bounds__(V == 1 ? 256 : 512, V == 1 ? 5 : 1)
 block_norm_kernel(const NormArgs a) {
-  __shared__ float2 part[2][2][kNormMaxWarps];
-  __shared__ int s_row[2][32];
-  __shared__ float s_w[2][32];
+  __shared__ float part[2][kNormMaxWarps];
   const int warps = blockDim.x >> 5;
   const int n8 = a.d >> 3;
-  int buf = 0;
-  for (long long t = blockIdx.x; t < a.T; t += gridDim.x, buf ^= 1) {
-    int nk = 0;
+  const long long t = blockIdx.x;
+  // the token's rows and gates, slot j's in lane j of every warp
+  int my_row = -1;
+  float my_gate = 1.f;
+  unsigned kept = 0;
+  if constexpr (COMBINE) {
+    const int lane = threadIdx.x & 31;
+    if (lane < a.k) {
+      my_row = __ldg(a.row_of + t * a.k + lane);
+      if (my_row >= a.rows_max) {
+        record_error(a.err, MOE_DEVERR_ROW);
+        my_row = -1;
+      }
+      if (a.topk_gate) my_gate = __ldg(a.topk_gate + t * a.k + lane);
+    }
+    kept = __ballot_sync(kFull, my_row >= 0);
+  }
+  Oct x[V], b[V];
+  f32x2 ss2 = both(0.f);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = threadIdx.x + v * blockDim.x;
+    x[v] = b[v] = oct_const(0.f);
+    const bool in_row = c < n8;
+    if (!COMBINE && !in_row) continue;
+    Raw8<RT> r;
+    if (in_row) r.load(a.r, t * a.d + c * 8);
     if constexpr (COMBINE) {
-      // the token's kept rows, in slot order
-      if (threadIdx.x < 32) {
-        int row = -1;
-        float g = 1.f;
-        if (threadIdx.x < a.k) {
-          row = __ldg(a.row_of + t * a.k + threadIdx.x);
-          if (row >= a.rows_max) { record_error(a.err, MOE_DEVERR_ROW); row = -1; }
-          if (a.topk_gate) g = __ldg(a.topk_gate + t * a.k + threadIdx.x);
+      // the kept slots in order, R at a time: all their loads, then the sums
+      constexpr int R = 4;
+      for (unsigned left = kept; left; left &= left - 1) {
+        Raw8<YT> in[R];
+        int slot[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          slot[j] = -1;
+          if (left) {
+            slot[j] = __ffs(left) - 1;
+            const long long row = __shfl_sync(kFull, my_row, slot[j]);   // by the whole warp
+            if (in_row) in[j].load(a.y, row * a.d + c * 8);
+            if (j + 1 < R) left &= left - 1;             // the loop drops the last one
+          }
         }
-        const unsigned kept = __ballot_sync(kFull, row >= 0);
-        s_row[buf][threadIdx.x] = -1;
-        __syncwarp();
-        if (row >= 0) {
-          const int at = __popc(kept & ((1u << threadIdx.x) - 1u));
-          s_row[buf][at] = row;
-          s_w[buf][at] = g;
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          if (slot[j] < 0) continue;
+          // without gates the factor is one: the product is exact, the sum rounds as an addition
+          const f32x2 g = both(__shfl_sync(kFull, my_gate, slot[j]));
+          const Oct o = in[j].oct();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) b[v].p[i] = fma2(g, o.p[i], b[v].p[i]);
         }
       }
-      __syncthreads();
-      while (nk < a.k && s_row[buf][nk] >= 0) ++nk;
+      if (!in_row) {
+        b[v] = oct_const(0.f);                           // sums of nothing that was loaded
+        continue;
+      }
+      if (a.shared_y) {
+        Raw8<YT> in;
+        in.load(a.shared_y, t * a.d + c * 8);
+        const Oct o = in.oct();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[v].p[i] = add2(b[v].p[i], o.p[i]);
+      }
+      if (a.y_out) store_oct<YT>(a.y_out, t * a.d + c * 8, b[v]);
+    } else if (a.y) {
+      Raw8<YT> in;
+      in.load(a.y, t * a.d + c * 8);
+      b[v] = in.oct();
     }
-    float x[V][8], b[V][8];
+    x[v] = r.oct();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ss2 = fma2(b[v].p[i], b[v].p[i], ss2);
+  }
+  f32x2 ry = both(1.f);
+  if (a.post) ry = both(inv_rms(block_sum(sum2(ss2), part[0], warps), a.inv_d, a.eps));
+  const float* gate = a.gate ? a.gate + (long long)((int)t / a.per_gate) * a.d : nullptr;
+  const f32x2 alpha = both(a.alpha);
+  ss2 = both(0.f);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = threadIdx.x + v * blockDim.x;
+    if (c >= n8) continue;
+    const Oct p = param8(a.post, c * 8), q = param8(gate, c * 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 br = mul2(mul2(mul2(b[v].p[i], ry), p.p[i]), q.p[i]);
+      x[v].p[i] = fma2(alpha, x[v].p[i], br);
+      ss2 = fma2(x[v].p[i], x[v].p[i], ss2);
+    }
+    if (a.x_out) store_oct<RT>(a.x_out, t * a.d + c * 8, x[v]);
+  }
+  if (a.pre) {
+    const f32x2 rx = both(inv_rms(block_sum(sum2(ss2), part[1], warps), a.inv_d, a.eps));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = threadIdx.x + v * blockDim.x;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[v][i] = b[v][i] = 0.f;
       if (c >= n8) continue;
-      load8<RT>(a.r, t * a.d + c * 8, x[v]);
-      if constexpr (COMBINE) {
-        for (int j0 = 0; j0 < nk; j0 += 4) {               // four rows in flight
-          Row8<YT> in[4];
+      Oct p = param8(a.pre, c * 8);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j0 + j < nk) in[j].load(a.y, (long long)s_row[buf][j0 + j] * a.d + c * 8);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j0 + j < nk) in[j].add(b[v], s_w[buf][j0 + j], a.topk_gate != nullptr);
-        }
-        if (a.shared_y) {
-          Row8<YT> in;
-          in.load(a.shared_y, t * a.d + c * 8);
-          in.add(b[v], 1.f, false);
-        }
-        if (a.y_out) store8<YT>(a.y_out, t * a.d + c * 8, b[v]);
-      } else {
-        if (a.y) load8<YT>(a.y, t * a.d + c * 8, b[v]);
-      }
-    }
-    float ry = 1.f;
-    if (a.post) {
-      float ss = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(b[v][i], b[v][i], ss);
-      ss = block_sum2(ss, 0.f, part[buf][0], warps).x;
-      ry = 1.f / sqrtf(ss / (float)a.d + a.eps);
-    }
-    const float* gate = a.gate ? a.gate + t / a.per_gate * a.d : nullptr;
-    float ss = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = threadIdx.x + v * blockDim.x;
-      if (c >= n8) continue;
-      float p[8];
-      if (a.post) {
-        param8(a.post, c * 8, p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[v][i] = b[v][i] * ry * p[i];
-      }
-      if (gate) {
-        param8(gate, c * 8, p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[v][i] *= p[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[v][i] = fmaf(a.alpha, x[v][i], b[v][i]);
-        ss = fmaf(x[v][i], x[v][i], ss);
-      }
-      if (a.x_out) store8<RT>(a.x_out, t * a.d + c * 8, x[v]);
-    }
-    if (a.pre) {
-      ss = block_sum2(ss, 0.f, part[buf][1], warps).x;
-      const float rx = 1.f / sqrtf(ss / (float)a.d + a.eps);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = threadIdx.x + v * blockDim.x;
-        if (c >= n8) continue;
-        float p[8];
-        param8(a.pre, c * 8, p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = x[v][i] * rx * p[i];
-        store8<NT>(a.n_out, t * a.d + c * 8, p);
-      }
+      for (int i = 0; i < 4; ++i) p.p[i] = mul2(mul2(x[v].p[i], rx), p.p[i]);
+      store_oct<NT>(a.n_out, t * a.d + c * 8, p);
     }
   }
 }
@@ -206,166 +235,323 @@ struct NormGradArgs {
   const float* pre;
   void* d_r;                  // [T, d]
   void* d_y;                  // [T, d] or null
-  float* p_post;              // [blocks, d] or null
+  float* d_gate;              // [G, d] or null
+  float* p_post;              // [blocks, d] or null: the blocks' sums
   float* p_pre;               // [blocks, d] or null
-  float* p_gate;              // [G, splits, d] or null
-  float alpha, eps;
-  int T, d, per_gate, splits, groups;
+  float* p_gate;              // [blocks, 2, d]: a block's part of a gate group it shares (edge_slot)
+  float alpha, eps, inv_d;
+  int T, d, per_gate, stages;
+  int* err;
 };
 
+constexpr int kGradStages = 4;
+
+// Tokens [row_begin(b), row_begin(b + 1)) are block b's.
+__host__ __device__ __forceinline__ int row_begin(long long T, int b, int blocks) { return (int)(T * b / blocks); }
+
+// Eight elements of a row in shared memory.
+template <typename T>
+__device__ __forceinline__ Oct row8(const uint8_t* base, int c) {
+  if constexpr (sizeof(T) == 2) {
+    return oct_bf16(*reinterpret_cast<const uint4*>(base + c * 16));
+  } else {
+    return oct_f32(*reinterpret_cast<const uint4*>(base + c * 32), *reinterpret_cast<const uint4*>(base + c * 32 + 16));
+  }
+}
+__device__ __forceinline__ void bulk_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// A block takes an equal run of tokens, whatever the gate groups.  Its rows arrive in a ring of
+// `stages` shared-memory buffers by bulk copies issued by thread 0, so that the next rows load
+// while a row is reduced; each phase reads what it needs from there, and u, h and the column sums
+// stay in registers.  A buffer is filled again once every thread is past the row after it (the
+// barrier of that row's first reduction), or, with one buffer, past the row itself.
+// gate * post of the current gate group waits in shared memory (each thread its own columns).
 template <typename YT, typename RT, typename NT, int V>
-__global__ void __launch_bounds__(V == 1 ? 256 : 512)
+__global__ void __launch_bounds__(V == 1 ? 256 : 512, V == 1 ? 3 : 1)
 block_norm_grad_kernel(const NormGradArgs a) {
+  extern __shared__ __align__(16) uint8_t nsm[];
   __shared__ float2 part[2][2][kNormMaxWarps];
+  __shared__ __align__(8) uint64_t s_bar[kGradStages];
+  __shared__ int s_abort;
   const int warps = blockDim.x >> 5;
   const int n8 = a.d >> 3;
-  float s_post[V][8], s_pre[V][8];
+  const uint32_t rb = (uint32_t)a.d * sizeof(RT), nb = (uint32_t)a.d * sizeof(NT), yb = (uint32_t)a.d * sizeof(YT);
+  // a stage: d_x, x_out, d_n, y, as far as they are given
+  const uint32_t o_x = a.d_x ? rb : 0, o_n = o_x + (a.pre ? rb : 0), o_y = o_n + (a.pre ? nb : 0);
+  const uint32_t stage_bytes = o_y + (a.y ? yb : 0);
+  uint8_t* s_w = nsm + (uint32_t)a.stages * stage_bytes;   // gate * post, fp32 [d]
+  const uint32_t bar0 = smem_u32(s_bar), buf0 = smem_u32(nsm);
+  volatile int* abort_flag = &s_abort;
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int s = 0; s < a.stages; ++s) mbar_init(bar0 + 8 * s, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int t0 = row_begin(a.T, blockIdx.x, gridDim.x), t1 = row_begin(a.T, blockIdx.x + 1, gridDim.x);
+  int load_t = t0, load_slot = 0;                          // thread 0: the next row to load
+  auto issue = [&]() {
+    if (load_t >= t1 || *abort_flag) return;
+    const uint32_t bar = bar0 + 8 * load_slot, dst = buf0 + (uint32_t)load_slot * stage_bytes;
+    const long long at = (long long)load_t * a.d;
+    mbar_expect_tx(bar, stage_bytes);
+    if (a.d_x) bulk_row(dst, static_cast<const RT*>(a.d_x) + at, rb, bar);
+    if (a.pre) {
+      bulk_row(dst + o_x, static_cast<const RT*>(a.x_out) + at, rb, bar);
+      bulk_row(dst + o_n, static_cast<const NT*>(a.d_n) + at, nb, bar);
+    }
+    if (a.y) bulk_row(dst + o_y, static_cast<const YT*>(a.y) + at, yb, bar);
+    ++load_t;
+    if (++load_slot == a.stages) load_slot = 0;
+  };
+  if (threadIdx.x == 0)
+    for (int s = 0; s < (a.stages > 1 ? a.stages - 1 : 1); ++s) issue();
+
+  Oct s_pre[V], s_uy[V];                                   // sum_t d_n xh; sum_t u yh over the gate group
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+  for (int v = 0; v < V; ++v) s_pre[v] = s_uy[v] = oct_const(0.f);
+  const f32x2 alpha = both(a.alpha);
+  int buf = 0, slot = 0;
+  uint32_t parity = 0;
+  int g = -1, g_end = t0;                                  // the current gate group, its last token + 1
+  bool any_post = false;
+  // the group's sums: d_gate = post * sum u yh (whole if the group is all this block's, else the
+  // block's part), and gate * the same onto the block's d_post
+  auto close_group = [&]() {
+    const bool whole = g * a.per_gate >= t0 && g_end <= t1;
+    const int edge = g * a.per_gate < t0 ? 0 : 1;          // it began before this block, or here
+    float* to = !a.d_gate ? nullptr
+                : whole   ? a.d_gate + (long long)g * a.d
+                          : a.p_gate + ((long long)blockIdx.x * 2 + edge) * a.d;
+    const float* gate = a.gate ? a.gate + (long long)g * a.d : nullptr;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_post[v][i] = s_pre[v][i] = 0.f;
-  int buf = 0;
-  // work item: split `sp` of gate group `g`, tokens [t0, t1)
-  for (long long item = blockIdx.x; item < (long long)a.groups * a.splits; item += gridDim.x) {
-    const int g = (int)(item / a.splits), sp = (int)(item - (long long)g * a.splits);
-    const int t0 = g * a.per_gate + (int)((long long)a.per_gate * sp / a.splits);
-    const int t1 = g * a.per_gate + (int)((long long)a.per_gate * (sp + 1) / a.splits);
-    float s_gate[V][8];
+    for (int v = 0; v < V; ++v) {
+      const int c = threadIdx.x + v * blockDim.x;
+      if (c >= n8) continue;
+      const Oct p = param8(a.post, c * 8), q = param8(gate, c * 8);
+      if (a.p_post) {
+        float* at = a.p_post + (long long)blockIdx.x * a.d + c * 8;
+        Oct o = oct_const(0.f);
+        if (any_post) o = oct_f32(*reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + 4));
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s_gate[v][i] = 0.f;
-    for (int t = t0; t < t1; ++t, buf ^= 1) {
-      const long long at = (long long)t * a.d;
-      float u[V][8], y[V][8], x[V][8], dn[V][8];
-      float xx = 0.f, gx = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = threadIdx.x + v * blockDim.x;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[v][i] = y[v][i] = x[v][i] = dn[v][i] = 0.f;
-        if (c >= n8) continue;
-        if (a.d_x) load8<RT>(a.d_x, at + c * 8, u[v]);
-        if (a.y) load8<YT>(a.y, at + c * 8, y[v]);
-        if (a.pre) {
-          load8<RT>(a.x_out, at + c * 8, x[v]);
-          load8<NT>(a.d_n, at + c * 8, dn[v]);
-          float p[8];
-          param8(a.pre, c * 8, p);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            xx = fmaf(x[v][i], x[v][i], xx);
-            gx = fmaf(p[i] * dn[v][i], x[v][i], gx);
-          }
-        }
+        for (int i = 0; i < 4; ++i) o.p[i] = fma2(q.p[i], s_uy[v].p[i], o.p[i]);
+        store_oct<float>(at, 0, o);
       }
-      if (a.pre) {
-        const float2 s = block_sum2(xx, gx, part[buf][0], warps);
-        const float rx = 1.f / sqrtf(s.x / (float)a.d + a.eps);
-        const float mx = s.y * rx / (float)a.d * rx;       // mean(g xh) / rms, for x
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int c = threadIdx.x + v * blockDim.x;
-          if (c >= n8) continue;
-          float p[8];
-          param8(a.pre, c * 8, p);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float xh = x[v][i] * rx;
-            s_pre[v][i] = fmaf(dn[v][i], xh, s_pre[v][i]);
-            u[v][i] += rx * (p[i] * dn[v][i]) - mx * xh;
-          }
-        }
-      }
+      for (int i = 0; i < 4; ++i) s_uy[v].p[i] = mul2(s_uy[v].p[i], p.p[i]);
+      if (to) store_oct<float>(to, c * 8, s_uy[v]);
+      s_uy[v] = oct_const(0.f);
+    }
+    any_post = true;
+  };
+  for (int t = t0; t < t1; ++t, buf ^= 1) {
+    if (t == g_end && a.y) {
+      if (g >= 0) close_group();
+      g = t / a.per_gate;
+      g_end = (g + 1) * a.per_gate;
       const float* gate = a.gate ? a.gate + (long long)g * a.d : nullptr;
-      float yy = 0.f, hy = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = threadIdx.x + v * blockDim.x;
         if (c >= n8) continue;
-        float o[8];
+        const Oct p = param8(a.post, c * 8);
+        Oct q = param8(gate, c * 8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = a.alpha * u[v][i];
-        store8<RT>(a.d_r, at + c * 8, o);
-        if (!a.y) continue;
-        float p[8], q[8];
-        if (a.post) param8(a.post, c * 8, p);
-        if (gate) param8(gate, c * 8, q);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float h = u[v][i] * (gate ? q[i] : 1.f) * (a.post ? p[i] : 1.f);
-          yy = fmaf(y[v][i], y[v][i], yy);
-          hy = fmaf(h, y[v][i], hy);
-        }
-      }
-      if (!a.y) continue;
-      float ry = 1.f, my = 0.f;
-      if (a.post) {
-        const float2 s = block_sum2(yy, hy, part[buf][1], warps);
-        ry = 1.f / sqrtf(s.x / (float)a.d + a.eps);
-        my = s.y * ry / (float)a.d * ry;                   // mean(h yh) / rms, for yh
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = threadIdx.x + v * blockDim.x;
-        if (c >= n8) continue;
-        float p[8], q[8], o[8];
-        if (a.post) param8(a.post, c * 8, p);
-        if (gate) param8(gate, c * 8, q);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float yh = y[v][i] * ry;
-          const float ug = u[v][i] * (gate ? q[i] : 1.f);
-          s_gate[v][i] = fmaf(u[v][i], a.post ? yh * p[i] : yh, s_gate[v][i]);
-          s_post[v][i] = fmaf(ug, yh, s_post[v][i]);
-          o[i] = a.post ? ry * (ug * p[i]) - my * yh : ug;
-        }
-        store8<YT>(a.d_y, at + c * 8, o);
+        for (int i = 0; i < 4; ++i) q.p[i] = mul2(q.p[i], p.p[i]);
+        store_oct<float>(s_w, c * 8, q);
       }
     }
-    if (a.p_gate) {
+    const long long at = (long long)t * a.d;
+    const uint8_t* st = nsm + (uint32_t)slot * stage_bytes;
+    Oct u[V];                                              // pre * d_n first
+    if (a.pre) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = threadIdx.x + v * blockDim.x;
-        if (c < n8) store8<float>(a.p_gate, item * a.d + c * 8, s_gate[v]);
+        u[v] = c < n8 ? param8(a.pre, c * 8) : oct_const(0.f);
       }
+    }
+    mbar_wait(bar0 + 8 * slot, parity, abort_flag, a.err);
+    if (++slot == a.stages) { slot = 0; parity ^= 1u; }
+    f32x2 rx = both(0.f), mx = both(0.f);
+    if (a.pre) {
+      f32x2 xx = both(0.f), gx = both(0.f);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = threadIdx.x + v * blockDim.x;
+        if (c >= n8) continue;
+        const Oct x = row8<RT>(st + o_x, c), dn = row8<NT>(st + o_n, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          u[v].p[i] = mul2(u[v].p[i], dn.p[i]);
+          xx = fma2(x.p[i], x.p[i], xx);
+          gx = fma2(u[v].p[i], x.p[i], gx);
+        }
+      }
+      const float2 s = block_sum2(sum2(xx), sum2(gx), part[buf][0], warps);
+      const float r = inv_rms(s.x, a.inv_d, a.eps);
+      rx = both(r);
+      mx = both(-(s.y * r * a.inv_d * r));              // minus mean(g xh) / rms, for xh
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) u[v] = oct_const(0.f);
+      __syncthreads();
+    }
+    if (a.stages > 1 && threadIdx.x == 0) issue();         // into the row before's buffer
+    f32x2 yy = both(0.f), hy = both(0.f);
+    Oct h[V];                                              // u gate post
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = threadIdx.x + v * blockDim.x;
+      if (c >= n8) continue;
+      if (a.pre) {
+        const Oct x = row8<RT>(st + o_x, c), dn = row8<NT>(st + o_n, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x2 xh = mul2(x.p[i], rx);
+          s_pre[v].p[i] = fma2(dn.p[i], xh, s_pre[v].p[i]);
+          u[v].p[i] = fma2(mx, xh, mul2(rx, u[v].p[i]));
+        }
+      }
+      if (a.d_x) {
+        const Oct dx = row8<RT>(st, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[v].p[i] = add2(u[v].p[i], dx.p[i]);
+      }
+      Oct o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o.p[i] = mul2(alpha, u[v].p[i]);
+      store_oct<RT>(a.d_r, at + c * 8, o);
+      if (!a.y) continue;
+      const Oct y = row8<YT>(st + o_y, c), w = row8<float>(s_w, c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[v].p[i] = mul2(u[v].p[i], w.p[i]);
+        yy = fma2(y.p[i], y.p[i], yy);
+        hy = fma2(h[v].p[i], y.p[i], hy);
+      }
+    }
+    if (a.y) {
+      // without a post-norm: 1 / rms = 1 and no mean
+      f32x2 ry = both(1.f), my = both(0.f);
+      if (a.post) {
+        const float2 s = block_sum2(sum2(yy), sum2(hy), part[buf][1], warps);
+        const float r = inv_rms(s.x, a.inv_d, a.eps);
+        ry = both(r);
+        my = both(-(s.y * r * a.inv_d * r));            // minus mean(h yh) / rms, for yh
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = threadIdx.x + v * blockDim.x;
+        if (c >= n8) continue;
+        const Oct y = row8<YT>(st + o_y, c);
+        Oct o = h[v];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x2 yh = mul2(y.p[i], ry);
+          s_uy[v].p[i] = fma2(u[v].p[i], yh, s_uy[v].p[i]);
+          if (a.post) o.p[i] = fma2(my, yh, mul2(ry, h[v].p[i]));
+        }
+        store_oct<YT>(a.d_y, at + c * 8, o);
+      }
+    }
+    if (a.stages == 1) {
+      __syncthreads();
+      if (threadIdx.x == 0) issue();
     }
   }
+  if (a.y && t1 > t0) close_group();
+  if (a.p_pre) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = threadIdx.x + v * blockDim.x;
-    if (c >= n8) continue;
-    if (a.p_post) store8<float>(a.p_post, (long long)blockIdx.x * a.d + c * 8, s_post[v]);
-    if (a.p_pre) store8<float>(a.p_pre, (long long)blockIdx.x * a.d + c * 8, s_pre[v]);
+    for (int v = 0; v < V; ++v) {
+      const int c = threadIdx.x + v * blockDim.x;
+      if (c < n8) store_oct<float>(a.p_pre, (long long)blockIdx.x * a.d + c * 8, s_pre[v]);
+    }
+  }
+  // after a timeout loads may be left in flight: let them land before the block's memory is reused
+  if (threadIdx.x == 0 && *abort_flag) {
+    const int loaded = load_t - t0;
+    for (int r = loaded > a.stages ? loaded - a.stages : 0; r < loaded; ++r)
+      mbar_wait_drain(bar0 + 8 * (r % a.stages), (uint32_t)(r / a.stages) & 1u, a.err);
   }
 }
 
-// out[r, c] = sum over the n partial rows of r, in order, in fp64.  32 columns x 8 slices of
-// the partial rows a block.
-struct ReduceJob {
-  const float* in;            // [rows, n, d]
-  float* out;                 // [rows, d]
-  int rows, n;
+// Column sums of partial rows in a fixed order: a block has 64 columns (two a lane) and 16 slices
+// of the rows, each added in fp32 (at most 30 rows), the slices in fp64.  blockIdx.y 0 and 1: the post and pre weights', over all blocks'
+// rows.  From 2 on: a gate group that two or more blocks share; its own part (slot 1) of the block
+// that begins it and the parts (slot 0) of the blocks after.  Those groups are found among the
+// groups, or among the blocks' last groups, whichever are fewer.
+struct ColumnArgs {
+  const float* post;          // [blocks, d], or null
+  const float* pre;
+  const float* gate;          // [blocks, 2, d], or null
+  float* d_post;
+  float* d_pre;
+  float* d_gate;
+  int blocks, d, T, per_gate, by_group;
 };
-__global__ void __launch_bounds__(256)
-column_sum_kernel(const ReduceJob j0, const ReduceJob j1, const ReduceJob j2, int d) {
-  __shared__ double s[8][32];
-  int r = blockIdx.y;
-  ReduceJob j = j0;
-  if (r >= j.rows) { r -= j.rows; j = j1; }
-  if (r >= j.rows) { r -= j.rows; j = j2; }
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
-  double acc = 0.0;
-  if (c < d) {
-    const float* p = j.in + (long long)r * j.n * d + c;
-    for (int i = part; i < j.n; i += 8) acc += (double)__ldg(p + (long long)i * d);
+constexpr int kSlices = 16;
+
+// The block that token t is in: the last one that begins at or before it.
+__device__ __forceinline__ int block_of(int t, int T, int blocks) {
+  return (int)(((long long)(t + 1) * blocks + T - 1) / T) - 1;
+}
+__global__ void __launch_bounds__(32 * kSlices)
+column_sum_kernel(const ColumnArgs a) {
+  __shared__ float s[kSlices][66];
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const float* in;
+  float* out;
+  long long first = 0, step = a.d;
+  int n = a.blocks;
+  if (blockIdx.y < 2) {
+    in = blockIdx.y ? a.pre : a.post;
+    out = blockIdx.y ? a.d_pre : a.d_post;
+    if (!in) return;
+  } else {
+    int b = blockIdx.y - 2;
+    const int g = a.by_group ? b : (row_begin(a.T, b + 1, a.blocks) - 1) / a.per_gate;
+    const int begin = g * a.per_gate, end = begin + a.per_gate;
+    if (a.by_group) b = block_of(begin, a.T, a.blocks);
+    if (begin < row_begin(a.T, b, a.blocks)) return;       // another block begins it
+    const int last = block_of(end - 1, a.T, a.blocks);
+    if (last == b) return;                                 // its block wrote the gradient
+    n = last - b + 1;
+    in = a.gate + (long long)b * 2 * a.d;
+    first = a.d;                                           // slot 1 of block b, then slots 0
+    step = 2LL * a.d;
+    out = a.d_gate + (long long)g * a.d;
   }
-  s[part][threadIdx.x & 31] = acc;
-  __syncthreads();
-  if (part == 0 && c < d) {
+  const int c = blockIdx.x * 64 + lane * 2;
+  float2 acc = make_float2(0.f, 0.f);
+  if (c < a.d) {
+    for (int i0 = part; i0 < n; i0 += 8 * kSlices) {
+      float2 f[8];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) acc += s[i][threadIdx.x & 31];
-    j.out[(long long)r * d + c] = (float)acc;
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + kSlices * k;
+        f[k] = i < n ? __ldg(reinterpret_cast<const float2*>(in + (i ? i * step : first) + c)) : make_float2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        acc.x += f[k].x;
+        acc.y += f[k].y;
+      }
+    }
+  }
+  s[part][lane * 2] = acc.x;
+  s[part][lane * 2 + 1] = acc.y;
+  __syncthreads();
+  const int cc = blockIdx.x * 64 + threadIdx.x;
+  if (threadIdx.x < 64 && cc < a.d) {
+    double sum = (double)s[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < kSlices; ++i) sum += (double)s[i][threadIdx.x];
+    out[cc] = (float)sum;
   }
 }
 
@@ -384,9 +570,8 @@ Shape row_shape(int n8) {
 template <typename YT, typename RT, typename NT, bool COMBINE>
 moe_status run_norm(const NormArgs& a, cudaStream_t s) {
   const Shape sh = row_shape(a.d / 8);
-  long long blocks = a.T;
-  const long long cap = (long long)num_sms() * 16;
-  if (blocks > cap) blocks = cap;
+  // a block for each row: they start as others end, so no wave of them is left half empty
+  const long long blocks = a.T;
   if (sh.V == 1) block_norm_kernel<YT, RT, NT, 1, COMBINE><<<(unsigned)blocks, sh.threads, 0, s>>>(a);
   else block_norm_kernel<YT, RT, NT, 2, COMBINE><<<(unsigned)blocks, sh.threads, 0, s>>>(a);
   return check_launch();
@@ -401,28 +586,44 @@ moe_status norm_types(const NormArgs& a, int r_dtype, int n_dtype, cudaStream_t 
                             : run_norm<YT, __nv_bfloat16, __nv_bfloat16, COMBINE>(a, s);
 }
 
-// Blocks of the backward pass and splits of a gate group: enough work items for two blocks a
-// multiprocessor, never more splits than tokens.
+// Blocks of the backward pass: what the device holds at once (a multiprocessor: three of 256
+// threads and one vector each, 512 threads of two, up to 16 small ones), at most one a token.
 struct GradPlan {
-  int splits, blocks;
+  int blocks, per_sm;
 };
-GradPlan grad_plan(int T, int G) {
+GradPlan grad_plan(int T, int d) {
   GradPlan p;
-  const int per = T / G;
-  const int want = 2 * num_sms();
-  p.splits = (want + G - 1) / G;
-  if (p.splits > per) p.splits = per;
-  const long long items = (long long)G * p.splits;
-  p.blocks = (int)(items < want ? items : want);
+  const Shape sh = row_shape(d / 8);
+  p.per_sm = (sh.V == 1 ? 768 : 512) / sh.threads;
+  if (p.per_sm < 1) p.per_sm = 1;
+  if (p.per_sm > 16) p.per_sm = 16;
+  const int want = p.per_sm * num_sms();
+  p.blocks = T < want ? T : want;
   return p;
 }
 
-template <typename YT, typename RT, typename NT>
-moe_status run_grad(const NormGradArgs& a, int blocks, cudaStream_t s) {
-  const Shape sh = row_shape(a.d / 8);
-  if (sh.V == 1) block_norm_grad_kernel<YT, RT, NT, 1><<<blocks, sh.threads, 0, s>>>(a);
-  else block_norm_grad_kernel<YT, RT, NT, 2><<<blocks, sh.threads, 0, s>>>(a);
+template <typename YT, typename RT, typename NT, int V>
+moe_status run_grad_v(NormGradArgs a, const GradPlan& p, int threads, cudaStream_t s) {
+  constexpr size_t kSmem = 222 * 1024;                     // a multiprocessor's, less the static part
+  static std::atomic<int> configured[kMaxDevices];
+  const moe_status st = ensure_smem_limit(configured, block_norm_grad_kernel<YT, RT, NT, V>, kSmem);
+  if (st != MOE_OK) return st;
+  const size_t row = (size_t)a.d * ((a.d_x ? sizeof(RT) : 0) + (a.pre ? sizeof(RT) + sizeof(NT) : 0) +
+                                    (a.y ? sizeof(YT) : 0));   // at most 128 KB: one always fits
+  const size_t w = a.y ? (size_t)a.d * sizeof(float) : 0;
+  const size_t room = kSmem / p.per_sm - 2048 - w;
+  a.stages = (int)(room / row);
+  if (a.stages > kGradStages) a.stages = kGradStages;
+  if (a.stages < 1) a.stages = 1;
+  block_norm_grad_kernel<YT, RT, NT, V><<<p.blocks, threads, a.stages * row + w, s>>>(a);
   return check_launch();
+}
+
+template <typename YT, typename RT, typename NT>
+moe_status run_grad(const NormGradArgs& a, const GradPlan& p, cudaStream_t s) {
+  const Shape sh = row_shape(a.d / 8);
+  if (sh.V == 1) return run_grad_v<YT, RT, NT, 1>(a, p, sh.threads, s);
+  return run_grad_v<YT, RT, NT, 2>(a, p, sh.threads, s);
 }
 
 }  // namespace
@@ -431,7 +632,7 @@ moe_status launch_block_norm(const void* r, int r_dtype, const void* y, int y_dt
                              const float* topk_gate, const void* shared_y, int k, long long rows_max, void* y_out,
                              const float* post, const float* gate, int G, float alpha, const float* pre, float eps,
                              int T, int d, void* x_out, void* n_out, int n_dtype, cudaStream_t s) {
-  NormArgs a{r, y, post, gate, pre, row_of, topk_gate, shared_y, y_out, x_out, n_out, rows_max, alpha, eps, T, d,
+  NormArgs a{r, y, post, gate, pre, row_of, topk_gate, shared_y, y_out, x_out, n_out, rows_max, alpha, eps, 1.f / (float)d, T, d,
              gate ? T / G : 1, k, err_ptr()};
   if (row_of)
     return y_dtype == MOE_F32 ? norm_types<float, true>(a, r_dtype, n_dtype, s)
@@ -440,46 +641,43 @@ moe_status launch_block_norm(const void* r, int r_dtype, const void* y, int y_dt
                             : norm_types<__nv_bfloat16, false>(a, r_dtype, n_dtype, s);
 }
 
-// Partial sums: the post and pre weights' by block, the gates' by work item (a gate group that
-// is one work item writes its gradient itself).
-size_t block_norm_grad_workspace_bytes(int T, int d, int G) {
-  const GradPlan p = grad_plan(T, G);
-  return ((size_t)2 * p.blocks + (p.splits > 1 ? (size_t)G * p.splits : 0)) * d * sizeof(float);
+// Each block's sums: the post and pre weights', and its parts of at most two gate groups that it
+// shares with its neighbours.
+size_t block_norm_grad_workspace_bytes(int T, int d) {
+  return (size_t)4 * grad_plan(T, d).blocks * d * sizeof(float);
 }
 
 moe_status launch_block_norm_backward(const void* d_x, const void* d_n, const void* x_out, const void* y, int y_dtype,
                                       int r_dtype, int n_dtype, const float* post, const float* gate, int G,
                                       float alpha, const float* pre, float eps, int T, int d, void* d_r, void* d_y,
                                       float* d_post, float* d_gate, float* d_pre, void* ws, cudaStream_t s) {
-  const GradPlan p = grad_plan(T, G);
+  const GradPlan p = grad_plan(T, d);
   float* w = static_cast<float*>(ws);
-  NormGradArgs a{d_x, d_n, x_out, y, post, gate, pre, d_r, d_y, d_post ? w : nullptr,
-                 d_pre ? w + (size_t)p.blocks * d : nullptr,
-                 d_gate && p.splits > 1 ? w + (size_t)2 * p.blocks * d : d_gate,
-                 alpha, eps, T, d, T / G, p.splits, G};
+  const size_t one = (size_t)p.blocks * d;
+  NormGradArgs a{d_x, d_n, x_out, y, post, gate, pre, d_r, d_y, d_gate, d_post ? w : nullptr, d_pre ? w + one : nullptr,
+                 w + 2 * one, alpha, eps, 1.f / (float)d, T, d, T / G, 1, err_ptr()};
   moe_status st;
   if (y_dtype == MOE_F32) {
     if (r_dtype == MOE_F32)
-      st = n_dtype == MOE_F32 ? run_grad<float, float, float>(a, p.blocks, s)
-                              : run_grad<float, float, __nv_bfloat16>(a, p.blocks, s);
+      st = n_dtype == MOE_F32 ? run_grad<float, float, float>(a, p, s)
+                              : run_grad<float, float, __nv_bfloat16>(a, p, s);
     else
-      st = n_dtype == MOE_F32 ? run_grad<float, __nv_bfloat16, float>(a, p.blocks, s)
-                              : run_grad<float, __nv_bfloat16, __nv_bfloat16>(a, p.blocks, s);
+      st = n_dtype == MOE_F32 ? run_grad<float, __nv_bfloat16, float>(a, p, s)
+                              : run_grad<float, __nv_bfloat16, __nv_bfloat16>(a, p, s);
   } else {
     if (r_dtype == MOE_F32)
-      st = n_dtype == MOE_F32 ? run_grad<__nv_bfloat16, float, float>(a, p.blocks, s)
-                              : run_grad<__nv_bfloat16, float, __nv_bfloat16>(a, p.blocks, s);
+      st = n_dtype == MOE_F32 ? run_grad<__nv_bfloat16, float, float>(a, p, s)
+                              : run_grad<__nv_bfloat16, float, __nv_bfloat16>(a, p, s);
     else
-      st = n_dtype == MOE_F32 ? run_grad<__nv_bfloat16, __nv_bfloat16, float>(a, p.blocks, s)
-                              : run_grad<__nv_bfloat16, __nv_bfloat16, __nv_bfloat16>(a, p.blocks, s);
+      st = n_dtype == MOE_F32 ? run_grad<__nv_bfloat16, __nv_bfloat16, float>(a, p, s)
+                              : run_grad<__nv_bfloat16, __nv_bfloat16, __nv_bfloat16>(a, p, s);
   }
   if (st != MOE_OK) return st;
-  ReduceJob jobs[3] = {{a.p_post, d_post, d_post ? 1 : 0, p.blocks},
-                       {a.p_pre, d_pre, d_pre ? 1 : 0, p.blocks},
-                       {a.p_gate, d_gate, d_gate && p.splits > 1 ? G : 0, p.splits}};
-  const int rows = jobs[0].rows + jobs[1].rows + jobs[2].rows;
-  if (rows == 0) return MOE_OK;
-  column_sum_kernel<<<dim3((d + 31) / 32, rows), 256, 0, s>>>(jobs[0], jobs[1], jobs[2], d);
+  if (!d_post && !d_gate && !d_pre) return MOE_OK;
+  const bool shared = d_gate && G < T;                     // a group of one token is never shared
+  const bool by_group = G <= p.blocks;
+  const ColumnArgs c{a.p_post, a.p_pre, a.p_gate, d_post, d_pre, d_gate, p.blocks, d, T, T / G, by_group};
+  column_sum_kernel<<<dim3((d + 63) / 64, 2 + (shared ? by_group ? G : p.blocks : 0)), 32 * kSlices, 0, s>>>(c);
   return check_launch();
 }
 

@@ -287,7 +287,7 @@ moe_status launch_block_norm(const void* r, int r_dtype, const void* y, int y_dt
                              const float* topk_gate, const void* shared_y, int k, long long rows_max, void* y_out,
                              const float* post, const float* gate, int G, float alpha, const float* pre, float eps,
                              int T, int d, void* x_out, void* n_out, int n_dtype, cudaStream_t s);
-size_t block_norm_grad_workspace_bytes(int T, int d, int G);
+size_t block_norm_grad_workspace_bytes(int T, int d);
 moe_status launch_block_norm_backward(const void* d_x, const void* d_n, const void* x_out, const void* y, int y_dtype,
                                       int r_dtype, int n_dtype, const float* post, const float* gate, int G,
                                       float alpha, const float* pre, float eps, int T, int d, void* d_r, void* d_y,

@@ -17,11 +17,13 @@
 // A masked logit (-inf or NaN) has gradient zero, a row of them only zeros.
 //
 // It reads each logit once and writes each gradient once: 8E bytes a token, bound by HBM with
-// the exponentials close behind.  One warp per token keeps the row in registers; the selected
-// experts' terms meet the dense ones through a row of shared memory.
+// the exponentials close behind.  One warp per token keeps the row, and of what it has computed
+// once (exponentials, scores) what the second pass needs, in registers.  Rows come and go through
+// two shared-memory buffers a warp by bulk copies, the next one on its way while one is worked
+// on; the selected experts' terms are added to the finished row there.
 #include <float.h>
 
-#include "common.cuh"
+#include "warp_rows.cuh"
 
 namespace moe {
 namespace {
@@ -39,21 +41,47 @@ __device__ __forceinline__ float wsum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
-__device__ __forceinline__ float clean_logit(float l) { return l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY; }
+// NaN counts as masked (-inf; fmaxf drops a NaN), +inf as the largest float.
+__device__ __forceinline__ float clean_logit(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
-// Score and derivative of the two scores that act on one logit alone; both 0 at -inf.  With
-// e = exp(-|l|): sigmoid = 1 / (1 + e) or e / (1 + e), and its derivative e / (1 + e)^2.
-__device__ __forceinline__ void score_grad(float l, int score, float* s, float* ds) {
-  const float e = expf(-fabsf(l));
-  const float r = 1.f / (1.f + e);
-  const float sig = l >= 0.f ? r : e * r;
-  if (score == MOE_SCORE_SIGMOID) {
-    *s = sig;
-    *ds = e * r * r;
+// exp(x) for x <= 0 within about 3 steps: 2^(x log2 e) by the exponential unit, the rounding of
+// the product and the rest of log2 e made up for to first order.  0 for -inf and below 2^-126.
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kL = 1.44269502f, kLlo = 1.92596299e-8f, kLn2 = 0.693147182f;
+  x = fmaxf(x, -200.f);
+  const float t = x * kL;
+  const float lo = fmaf(x, kLlo, fmaf(x, kL, -t));
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return fmaf(r, lo * kLn2, r);
+}
+__device__ __forceinline__ float rcp_fast(float x) {       // x in [1, 2] or a normal number: 1 step
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+struct Sig {
+  float e, r;                                              // exp(-|l|), 1 / (1 + e)
+};
+__device__ __forceinline__ Sig sig_parts(float l) {
+  Sig s;
+  s.e = exp_neg(-fabsf(l));
+  s.r = rcp_fast(1.f + s.e);
+  return s;
+}
+// Score and derivative of the two scores that act on one logit alone; both 0 at -inf.
+// sigmoid = r or e r, its derivative e r^2; sqrt(softplus)' = sigmoid / (2 sqrt(softplus)).
+template <int SCORE>
+__device__ __forceinline__ void score_grad(float l, float* s, float* ds) {
+  const Sig p = sig_parts(l);
+  if (SCORE == MOE_SCORE_SIGMOID) {
+    *s = l >= 0.f ? p.r : p.e * p.r;
+    *ds = p.e * p.r * p.r;
   } else {
-    const float root = sqrtf(fmaxf(l, 0.f) + log1pf(e));
+    const float sig = l >= 0.f ? p.r : p.e * p.r;
+    const float root = sqrtf(fmaxf(l, 0.f) + log1pf(p.e));
     *s = root;
-    *ds = root > 0.f ? sig / (2.f * root) : 0.f;
+    *ds = root > 0.f ? __fdividef(sig, 2.f * root) : 0.f;
   }
 }
 
@@ -63,47 +91,68 @@ struct GradArgs {
   const float* d_gate;
   const float* load;
   float* d_logits;
-  int T, E, k, score, renorm;
+  int T, E, k, renorm;
   float scale, aux, z;     // aux = aux_coef * E / T, z = 2 * z_coef / T
   int* err;
 };
 
-// NV: vectors of four logits a lane holds (VEC), or single ones.
-template <int NV, bool VEC>
-__global__ void __launch_bounds__(32 * kGradWarps)
+// What reaches every expert: nothing (only the selected ones' gradients are not zero), one dense
+// term (softmax: any mix of them; others: the load-balancing loss), or the z-loss's softmax next
+// to another score.
+constexpr int kSparse = 0, kDense = 1, kBoth = 2;
+
+__device__ __forceinline__ void bulk_store_row(float* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// NV: chunks of four logits a lane can hold.  BULK: rows come and go through the warp's two
+// shared-memory buffers by bulk copies (rows of whole 16-byte pieces); otherwise single loads and
+// stores, and one buffer to put the row together in.
+template <int NV, bool BULK, int SCORE, int TERMS>
+__global__ void __launch_bounds__(32 * kGradWarps, NV <= 4 ? 4 : TERMS == kBoth ? 2 : 3)
 route_grad_kernel(const GradArgs a) {
-  constexpr int W = VEC ? 4 : 1;
-  constexpr int N = NV * W;
-  extern __shared__ __align__(16) float rsm[];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  constexpr int N = 4 * NV;
+  constexpr bool SM = SCORE == MOE_SCORE_SOFTMAX;
+  extern __shared__ __align__(16) uint8_t rsm[];
+  __shared__ __align__(8) uint64_t s_bar[kGradWarps][2];
+  __shared__ int s_abort;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int E = a.E, k = a.k;
-  float* add = rsm + (size_t)w * ((E + 3) / 4 * 4);       // the selected experts' terms; zero in between
-  for (int e = lane; e < E; e += 32) add[e] = 0.f;
-  __syncwarp();
-  auto at = [&](int i) { return VEC ? 4 * (lane + 32 * (i / 4)) + i % 4 : lane + 32 * i; };
-  const bool sm = a.score == MOE_SCORE_SOFTMAX;
-  const bool gates = a.d_gate != nullptr;
-  const bool aux = a.aux != 0.f, zl = a.z != 0.f;
-  const bool need_p = (sm && (aux || (gates && !a.renorm))) || zl;   // the full softmax
-  const bool need_s = !sm && aux;                                    // every expert's score
-  const long long nw = (long long)gridDim.x * kGradWarps;
-  for (long long t = (long long)blockIdx.x * kGradWarps + w; t < a.T; t += nw) {
-    const float* l = a.logits + t * E;
-    float v[N];
+  const uint32_t pitch = (uint32_t)(E + 3) / 4 * 16;       // bytes of a buffer
+  volatile int* abort_flag = &s_abort;
+  if (threadIdx.x == 0) s_abort = 0;
+  __syncthreads();
+  WarpRows rows;
+  uint8_t* mine = rsm + (size_t)w * (BULK ? 2 : 1) * pitch;
+  if (BULK) rows.init(s_bar[w], mine, pitch, lane);
+  auto at = [&](int i) { return BULK ? 4 * (lane + 32 * (i >> 2)) + (i & 3) : lane + 32 * i; };
+  auto fetch = [&](const float* p, int i, float (&f)[4], float none) {
+    if constexpr (BULK) {
+      float4 q = make_float4(none, none, none, none);
+      if (at(i) < E) q = *reinterpret_cast<const float4*>(p + at(i));
+      f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; i += W) {
-      const int e = at(i);
-      if constexpr (VEC) {
-        const float4 q = e < E ? __ldg(reinterpret_cast<const float4*>(l + e))
-                               : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        v[i] = clean_logit(q.x); v[i + 1] = clean_logit(q.y);
-        v[i + 2] = clean_logit(q.z); v[i + 3] = clean_logit(q.w);
-      } else {
-        v[i] = e < E ? clean_logit(__ldg(l + e)) : -INFINITY;
-      }
+      for (int c = 0; c < 4; ++c) f[c] = at(i + c) < E ? __ldg(p + at(i + c)) : none;
     }
+  };
+  const bool gates = a.d_gate != nullptr;
+  constexpr bool DENSE = TERMS != kSparse;
+  constexpr bool need_p = SM ? DENSE : TERMS == kBoth;     // the full softmax
+  const bool aux = DENSE && a.aux != 0.f;
+  const int used = 4 * ((E + 127) / 128);                  // logits of a lane that exist (warp-uniform)
+  const long long nw = (long long)gridDim.x * warps;
+  const long long first = (long long)blockIdx.x * warps + w;
+  unsigned it = 0, loaded = 0;                             // tokens done; rows asked for
+  if (BULK && lane == 0 && first < a.T) rows.load(loaded++, a.logits + first * E);
+  for (long long t = first; t < a.T; t += nw, ++it) {
+    const float* l = a.logits + t * E;
+    float* out = reinterpret_cast<float*>(mine);           // where the row is put together
     // -------------------------------------------------- the selected experts, a lane each
-    float p_dot = 0.f;                                     // softmax: sum_j p_{i_j} u_j
     int sel = -1;
     float lf = -INFINITY, u = 0.f;
     if (gates && lane < k) {
@@ -112,8 +161,27 @@ route_grad_kernel(const GradArgs a) {
         record_error(a.err, MOE_DEVERR_EXPERT_ID);
         sel = -1;
       } else {
-        lf = clean_logit(__ldg(l + sel));
         u = a.scale * __ldg(a.d_gate + t * k + lane);
+      }
+    }
+    if constexpr (BULK) {
+      if (!rows.wait(it, abort_flag, a.err)) break;
+      out = rows.row(it);
+      l = out;
+      if (lane == 0 && t + nw < a.T) {
+        bulk_wait_read();                                  // the row before has left the other buffer
+        rows.load(loaded++, a.logits + (t + nw) * E);
+      }
+    }
+    if (sel >= 0) lf = clean_logit(l[sel]);
+    float v[N];                                            // logits; softmax: exp(l - max) further down
+    if (DENSE) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        float f[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (i < used) fetch(l, i, f, -INFINITY);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[i + c] = clean_logit(f[c]);
       }
     }
     float m = -INFINITY, lse = 0.f, iz = 0.f;
@@ -123,28 +191,36 @@ route_grad_kernel(const GradArgs a) {
       m = wmax(m);
       if (m > -INFINITY) {
         float zs = 0.f;
+        // a masked logit's exponential is 0, and so are all its terms; softmax keeps them in v
 #pragma unroll
-        for (int i = 0; i < N; ++i) zs += expf(v[i] - m);
+        for (int i = 0; i < N; ++i) {
+          if ((i & ~3) >= used) continue;
+          const float x = exp_neg(v[i] - m);
+          if (SM) v[i] = x;
+          zs += x;
+        }
         zs = wsum(zs);
         iz = 1.f / zs;
         lse = m + logf(zs);
+      } else if (SM) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.f;
       }
     }
-    const bool live = m > -INFINITY;
+    float dk = 0.f, p_dot = 0.f;                           // p_dot, softmax: sum_j p_{i_j} u_j
     if (gates) {
-      float dk = 0.f;
-      if (sm && a.renorm) {
+      if (SM && a.renorm) {
         const float mk = wmax(lf);
         const float ex = lf > -INFINITY ? expf(lf - mk) : 0.f;
         const float tot = wsum(ex);
         const float q = tot > 0.f ? ex / tot : 0.f;
         dk = q * (u - wsum(q * u));
-      } else if (sm) {
+      } else if (SM) {
         dk = lf > -INFINITY ? expf(lf - m) * iz * u : 0.f;
         p_dot = wsum(dk);
       } else {
         float s = 0.f, ds = 0.f;
-        if (lf > -INFINITY) score_grad(lf, a.score, &s, &ds);
+        if (lf > -INFINITY) score_grad<SCORE>(lf, &s, &ds);
         if (a.renorm) {
           const float tot = wsum(s), dot = wsum(s * u);
           dk = tot > 0.f ? ds * (u - dot / tot) / tot : 0.f;
@@ -152,90 +228,128 @@ route_grad_kernel(const GradArgs a) {
           dk = ds * u;
         }
       }
-      if (sel >= 0 && dk != 0.f) atomicAdd(add + sel, dk);   // a repeated expert's terms add up
-      __syncwarp();
     }
     // -------------------------------------------------- the dense terms
     float fp = 0.f, tot = 0.f;
+    float s_[SM ? 1 : N];                                  // the other scores' values
     if (aux) {
 #pragma unroll
-      for (int i = 0; i < N; i += W) {
-        const int e = at(i);
-        float f[W];
-        if constexpr (VEC) {
-          const float4 q = e < E ? __ldg(reinterpret_cast<const float4*>(a.load + e)) : make_float4(0, 0, 0, 0);
-          f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
-        } else {
-          f[0] = e < E ? __ldg(a.load + e) : 0.f;
-        }
+      for (int i = 0; i < N; i += 4) {
+        if (i >= used) continue;
+        float f[4];
+        fetch(a.load, i, f, 0.f);
 #pragma unroll
-        for (int c = 0; c < W; ++c) {
-          if (!(v[i + c] > -INFINITY)) continue;
-          float s, ds;
-          if (sm) s = expf(v[i + c] - m) * iz;
-          else score_grad(v[i + c], a.score, &s, &ds);
-          fp = fmaf(f[c], s, fp);
-          tot += s;
+        for (int c = 0; c < 4; ++c) {
+          if (SM) {
+            fp = fmaf(f[c], v[i + c], fp);
+          } else {
+            float s, ds;
+            score_grad<SCORE>(v[i + c], &s, &ds);
+            s_[SM ? 0 : i + c] = SCORE == MOE_SCORE_SIGMOID ? s : ds;
+            fp = fmaf(f[c], s, fp);
+            tot += s;
+          }
         }
       }
       fp = wsum(fp);
-      if (need_s) {
+      if (SM) {
+        fp *= iz;
+      } else {
         tot = wsum(tot);
         fp = tot > 0.f ? fp / tot : 0.f;
       }
     }
-    const float it = need_s && tot > 0.f ? a.aux / tot : 0.f;
-    const float zc = a.z * lse;
-    float* out = a.d_logits + t * E;
+    const float inv = !SM && aux && tot > 0.f ? a.aux / tot : 0.f;
+    // softmax: dl = p (zc - p_dot + aux (f - fp)); the constant parts together
+    const float flat = a.z * lse - p_dot - (SM && aux ? a.aux * fp : 0.f);
+    __syncwarp();                                          // every lane has read the row
 #pragma unroll
-    for (int i = 0; i < N; i += W) {
-      const int e = at(i);
-      if (e >= E) continue;
-      float o[W], f[W];
-      if constexpr (VEC) {
-        const float4 q = *reinterpret_cast<const float4*>(add + e);
-        o[0] = q.x; o[1] = q.y; o[2] = q.z; o[3] = q.w;
-        if (gates) *reinterpret_cast<float4*>(add + e) = make_float4(0, 0, 0, 0);
-        const float4 r = aux ? __ldg(reinterpret_cast<const float4*>(a.load + e)) : make_float4(0, 0, 0, 0);
-        f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
+    for (int i = 0; i < N; i += 4) {
+      if (i >= used || at(i) >= E) continue;
+      float o[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
+      if (aux) fetch(a.load, i, f, 0.f);
+      if (DENSE) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float x = v[i + c];
+          if (SM) {
+            o[c] = x * iz * (aux ? fmaf(a.aux, f[c], flat) : flat);
+          } else {
+            if (need_p && iz > 0.f) o[c] = exp_neg(x - m) * iz * flat;
+            if (aux) {
+              const float s = s_[SM ? 0 : i + c];
+              const float ds = SCORE == MOE_SCORE_SIGMOID ? fmaf(-s, s, s) : s;
+              o[c] = fmaf(inv * ds, f[c] - fp, o[c]);
+            }
+          }
+        }
+      }
+      if constexpr (BULK) {
+        *reinterpret_cast<float4*>(out + at(i)) = make_float4(o[0], o[1], o[2], o[3]);
       } else {
-        o[0] = add[e];
-        if (gates) add[e] = 0.f;
-        f[0] = aux ? __ldg(a.load + e) : 0.f;
-      }
 #pragma unroll
-      for (int c = 0; c < W; ++c) {
-        const float x = v[i + c];
-        if (!(x > -INFINITY)) { o[c] = 0.f; continue; }
-        if (need_p && live) {
-          const float p = expf(x - m) * iz;
-          float dense = zc - p_dot;
-          if (sm && aux) dense += a.aux * (f[c] - fp);
-          o[c] = fmaf(p, dense, o[c]);
-        }
-        if (need_s) {
-          float s, ds;
-          score_grad(x, a.score, &s, &ds);
-          o[c] = fmaf(it * ds, f[c] - fp, o[c]);
-        }
+        for (int c = 0; c < 4; ++c)
+          if (at(i + c) < E) out[at(i + c)] = o[c];
       }
-      if constexpr (VEC)
-        *reinterpret_cast<float4*>(out + e) = make_float4(o[0], o[1], o[2], o[3]);
-      else
-        out[e] = o[0];
     }
     __syncwarp();
+    if (sel >= 0 && lf > -INFINITY) atomicAdd(out + sel, dk);   // a repeated expert's terms add up
+    if constexpr (BULK) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) bulk_store_row(a.d_logits + t * E, smem_u32(out), pitch);
+    } else {
+      __syncwarp();
+      for (int e = lane; e < E; e += 32) a.d_logits[t * E + e] = out[e];
+      __syncwarp();
+    }
+  }
+  if (BULK && lane == 0) {
+    rows.drain(it, loaded, a.err);                         // after a timeout: what is still in flight
+    bulk_wait_all();
   }
 }
 
-template <int NV, bool VEC>
+template <int NV, bool BULK, int SCORE, int TERMS>
 moe_status run_grad(const GradArgs& a, cudaStream_t s) {
-  const size_t smem = (size_t)kGradWarps * ((a.E + 3) / 4 * 4) * sizeof(float);   // at most 32 KB
-  long long blocks = ((long long)a.T + kGradWarps - 1) / kGradWarps;
-  const long long cap = (long long)num_sms() * 8;
+  const int sms = num_sms();
+  int warps = (a.T + sms - 1) / sms;
+  if (warps > kGradWarps) warps = kGradWarps;
+  constexpr size_t kMost = (size_t)kGradWarps * 2 * 4096;  // two rows of 1024 a warp
+  static std::atomic<int> configured[kMaxDevices];
+  const moe_status st = ensure_smem_limit(configured, route_grad_kernel<NV, BULK, SCORE, TERMS>, kMost);
+  if (st != MOE_OK) return st;
+  const size_t smem = (size_t)warps * (BULK ? 2 : 1) * ((a.E + 3) / 4 * 16);
+  long long blocks = ((long long)a.T + warps - 1) / warps;
+  const long long cap = (long long)sms * (NV <= 4 ? 4 : TERMS == kBoth ? 2 : 3);   // what a multiprocessor holds
   if (blocks > cap) blocks = cap;
-  route_grad_kernel<NV, VEC><<<(unsigned)blocks, 32 * kGradWarps, smem, s>>>(a);
+  route_grad_kernel<NV, BULK, SCORE, TERMS><<<(unsigned)blocks, 32 * warps, smem, s>>>(a);
   return check_launch();
+}
+
+template <int SCORE, int TERMS>
+moe_status grad_size(const GradArgs& a, bool bulk, cudaStream_t s) {
+  const int nv = (a.E + 127) / 128;                        // at most 8
+  if (bulk) {
+    if (nv <= 1) return run_grad<1, true, SCORE, TERMS>(a, s);
+    if (nv <= 2) return run_grad<2, true, SCORE, TERMS>(a, s);
+    if (nv <= 4) return run_grad<4, true, SCORE, TERMS>(a, s);
+    return run_grad<8, true, SCORE, TERMS>(a, s);
+  }
+  if (nv <= 1) return run_grad<1, false, SCORE, TERMS>(a, s);
+  if (nv <= 4) return run_grad<4, false, SCORE, TERMS>(a, s);
+  return run_grad<8, false, SCORE, TERMS>(a, s);
+}
+
+template <int SCORE>
+moe_status grad_terms(const GradArgs& a, bool bulk, cudaStream_t s) {
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+    const bool dense = a.aux != 0.f || a.z != 0.f || (a.d_gate && !a.renorm);
+    return dense ? grad_size<SCORE, kDense>(a, bulk, s) : grad_size<SCORE, kSparse>(a, bulk, s);
+  } else {
+    if (a.z != 0.f) return grad_size<SCORE, kBoth>(a, bulk, s);
+    return a.aux != 0.f ? grad_size<SCORE, kDense>(a, bulk, s) : grad_size<SCORE, kSparse>(a, bulk, s);
+  }
 }
 
 }  // namespace
@@ -243,21 +357,12 @@ moe_status run_grad(const GradArgs& a, cudaStream_t s) {
 moe_status launch_route_backward(const float* logits, const int32_t* topk_idx, const float* d_gate, int T, int E,
                                  int k, int score, int renorm, float scale, const float* load, float aux_coef,
                                  float z_coef, float* d_logits, cudaStream_t s) {
-  GradArgs a{logits, topk_idx, d_gate, load, d_logits, T, E, k, score, renorm, scale,
+  GradArgs a{logits, topk_idx, d_gate, load, d_logits, T, E, k, renorm, scale,
              (float)((double)aux_coef * E / T), (float)(2.0 * (double)z_coef / T), err_ptr()};
-  const bool vec = E % 4 == 0 && aligned16(logits) && aligned16(d_logits) && aligned16(load);
-  if (vec) {
-    const int nv = (E / 4 + 31) / 32;                      // at most 8
-    if (nv <= 1) return run_grad<1, true>(a, s);
-    if (nv <= 2) return run_grad<2, true>(a, s);
-    if (nv <= 4) return run_grad<4, true>(a, s);
-    if (nv <= 7) return run_grad<7, true>(a, s);
-    return run_grad<8, true>(a, s);
-  }
-  const int nv = (E + 31) / 32;                            // at most 32
-  if (nv <= 2) return run_grad<2, false>(a, s);
-  if (nv <= 8) return run_grad<8, false>(a, s);
-  return run_grad<32, false>(a, s);
+  const bool bulk = E % 4 == 0 && aligned16(logits) && aligned16(d_logits) && aligned16(load);
+  if (score == MOE_SCORE_SOFTMAX) return grad_terms<MOE_SCORE_SOFTMAX>(a, bulk, s);
+  if (score == MOE_SCORE_SIGMOID) return grad_terms<MOE_SCORE_SIGMOID>(a, bulk, s);
+  return grad_terms<MOE_SCORE_SQRT_SOFTPLUS>(a, bulk, s);
 }
 
 }  // namespace moe

@@ -20,12 +20,17 @@
 //     lane maxima is a lower bound of the k-th largest key, so everything below it (less
 //     2 delta) is out.  What is left, about k to 2k experts, gets one lane each: its key in
 //     fp64, and its rank by counting the larger ones.  No round per selected expert.
-//   - Where fp32 cannot decide (two groups within 2 delta at the border, more than 32 experts
-//     left, softmax keys within 2 delta), the warp does the token again in fp64 alone.
+//   - Where the border between kept and dropped groups is closer than fp32 holds, the experts
+//     that can be among the groups' two largest are evaluated in fp64.  Where fp32 cannot decide
+//     at all (more than 32 experts left, softmax keys within 2 delta), the warp does the token
+//     again in fp64 alone.
+//   - Rows of whole 16-byte pieces come by bulk copies, one token ahead.
 // So every selection is the fp64 one; the fp32 pass only discards what cannot be selected.
 #include <float.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
+#include "warp_rows.cuh"
 
 namespace moe {
 namespace {
@@ -54,125 +59,190 @@ __device__ __forceinline__ double wmax_d(double v) {
   return v;
 }
 
-// A logit as the routing takes it: NaN counts as masked (-inf), +inf as the largest float.
-__device__ __forceinline__ float clean_logit(float l) { return l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY; }
+// A logit as the routing takes it: NaN counts as masked (-inf; fmaxf drops a NaN), +inf as the
+// largest float.
+__device__ __forceinline__ float clean_logit(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
 __device__ __forceinline__ double score64(double l, int score) {
   if (score == MOE_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-l));
   return sqrt(fmax(l, 0.0) + log1p(exp(-fabs(l))));
 }
 
-// log(1 + e) for 0 <= e <= 1 as 2 atanh(z), z = e / (2 + e) <= 1/3: the series in z^2 <= 1/9
-// to z^15 leaves 2 z^17 / 17 < 1e-9 of it out, and keeps the relative error of a small e.
-__device__ __forceinline__ float log1p_unit(float e) {
-  const float z = __fdividef(e, 2.f + e), q = z * z;
-  float s = 1.f / 15.f;
-  s = fmaf(s, q, 1.f / 13.f);
-  s = fmaf(s, q, 1.f / 11.f);
-  s = fmaf(s, q, 1.f / 9.f);
-  s = fmaf(s, q, 1.f / 7.f);
-  s = fmaf(s, q, 1.f / 5.f);
-  s = fmaf(s, q, 1.f / 3.f);
-  s = fmaf(s, q, 1.f);
-  return 2.f * z * s;
+// The units' own exponential (base 2), reciprocal and square root, subnormals flushed: each is
+// within 2 steps of its result.
+__device__ __forceinline__ float ex2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
-// fp32 score for discarding, with the fast exponential: its error grows with |l| (2 + 1.2 |l|
-// steps), but for l < -1 the score itself falls faster, so over a row the error stays below
-// the largest score times 2e-6 + 2.4e-7 |l of the largest score|.
-__device__ __forceinline__ float score32(float l, int score) {
-  if (score == MOE_SCORE_SIGMOID) return __fdividef(1.f, 1.f + __expf(-l));
-  return sqrtf(fmaxf(l, 0.f) + log1p_unit(__expf(-fabsf(l))));
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.44269504f;
+
+// log(1 + e) on [0, 1] as e times a degree-7 polynomial fitted here for the least largest
+// relative error (2.4e-7): it keeps the relative precision of a small e.
+__device__ __forceinline__ f32x2 log1p_unit(f32x2 e) {
+  f32x2 s = fma2(both(-0.00853919890f), e, both(0.0440895967f));
+  s = fma2(s, e, both(-0.107681662f));
+  s = fma2(s, e, both(0.177452385f));
+  s = fma2(s, e, both(-0.244954616f));
+  s = fma2(s, e, both(0.332754791f));
+  s = fma2(s, e, both(-0.499974042f));
+  s = fma2(s, e, both(0.999999821f));
+  return mul2(s, e);
+}
+// fp32 scores of two logits for discarding; 0 at -inf.  The exponent l log2(e) is rounded, so the
+// error grows with |l| (2 + 1.2 |l| steps), but for l < -1 the score itself falls faster: over a
+// row the error stays below the largest score times 2e-6 + 2.4e-7 |l of the largest score|,
+// as long as that score is far above the flushed subnormals.
+template <int SCORE>
+__device__ __forceinline__ float2 score32(float x, float y) {
+  if (SCORE == MOE_SCORE_SIGMOID)
+    return make_float2(rcp_fast(1.f + ex2_fast(x * -kLog2e)), rcp_fast(1.f + ex2_fast(y * -kLog2e)));
+  const f32x2 e = pack2(ex2_fast(fabsf(x) * -kLog2e), ex2_fast(fabsf(y) * -kLog2e));
+  const float2 s = unpack2(add2(log1p_unit(e), pack2(fmaxf(x, 0.f), fmaxf(y, 0.f))));
+  return make_float2(sqrt_fast(s.x), sqrt_fast(s.y));
 }
 
 struct Pick {
   int idx;        // lane j < k: the j-th selected expert
   double m, z;    // softmax: largest unmasked logit and sum of exp(l - m), if they were asked for
+  double s;       // sigmoid, sqrt(softplus): the selected expert's score
 };
 
-// The whole selection of one token in fp64, by the warp.  Each lane keeps the keys of experts
-// lane, lane + 32, ... in local memory; k rounds of an arg-max.
-__device__ __noinline__ Pick route_token_fp64(const float* __restrict__ l, const float* __restrict__ bias, int E,
-                                              int n, int G, int kept, int k, int score, int top2) {
+struct GroupArgs {
+  const float* logits;
+  const float* bias;
+  int32_t* topk_idx;
+  float* topk_gate;
+  int T, E, k, G, n, kept, team, chunks, top2, renorm;
+  float scale;
+  int* err;
+};
+
+// The whole selection of one token in fp64, by the warp.  A lane keeps the keys of its part of its
+// group (every team-th expert) in local memory and its best one at hand; k rounds of an arg-max
+// over the lanes follow.  One token here holds up its warp for some 15 us.
+template <int SCORE>
+__device__ __noinline__ Pick route_token_fp64(const GroupArgs& a, const float* l) {
   const int lane = threadIdx.x & 31;
-  double key[32];
+  const int L = a.team, g = lane / L, tl = lane - g * L;
+  const bool in_g = g < a.G;
+  const int count = in_g && tl < a.n ? (a.n - tl + L - 1) / L : 0;   // at most 64
+  const int e0 = g * a.n + tl;
+  double key[64];
   Pick out;
   out.m = 0.0;
   out.z = 1.0;
-  if (score == MOE_SCORE_SOFTMAX) {
+  if (SCORE == MOE_SCORE_SOFTMAX) {
     double m = -INFINITY, z = 0.0;
-#pragma unroll 1
-    for (int e = lane; e < E; e += 32) m = fmax(m, (double)clean_logit(__ldg(l + e)));
+    for (int i = 0; i < count; ++i) m = fmax(m, (double)clean_logit(l[e0 + i * L]));
     m = wmax_d(m);
     if (m > -INFINITY) {
-#pragma unroll 1
-      for (int e = lane; e < E; e += 32) z += exp((double)clean_logit(__ldg(l + e)) - m);
+#pragma unroll 2
+      for (int i = 0; i < count; ++i) z += exp((double)clean_logit(l[e0 + i * L]) - m);
       z = wsum_d(z);
       out.m = m;
       out.z = z;
     }
   }
-  auto value = [&](int e, float lf) {                      // score (+ bias); only for lf > -inf
-    const double s = score == MOE_SCORE_SOFTMAX ? exp((double)lf - out.m) / out.z : score64((double)lf, score);
-    return bias ? s + (double)__ldg(bias + e) : s;
-  };
-#pragma unroll 1
-  for (int i = 0, e = lane; e < E; ++i, e += 32) {
-    const float lf = clean_logit(__ldg(l + e));
-    double v = (double)lf;
-    if (bias && lf > -INFINITY) {
-      v = value(e, lf);
-      if (v != v) v = -INFINITY;
+  // keys; the group's two largest values; the lane's best key (the first of equal ones)
+  const bool scored = a.bias || a.top2;
+  double v1 = -INFINITY, v2 = -INFINITY, bk = -INFINITY;
+  int bi = -1;
+#pragma unroll 2
+  for (int i = 0; i < count; ++i) {
+    const float lf = clean_logit(l[e0 + i * L]);
+    double k = (double)lf, v = k;
+    if (scored && lf > -INFINITY) {
+      v = SCORE == MOE_SCORE_SOFTMAX ? exp(k - out.m) / out.z : score64(k, SCORE);
+      if (a.bias) {
+        v += (double)__ldg(a.bias + e0 + i * L);
+        if (v != v) v = -INFINITY;
+        k = v;
+      }
     }
-    key[i] = v;
+    if (!a.top2) v = k;
+    key[i] = k;
+    if (v > v1) { v2 = v1; v1 = v; } else if (v > v2) v2 = v;
+    if (bi < 0 || k > bk) { bk = k; bi = i; }
   }
-  // group values, group g's in lane g
-  double mine = -INFINITY;
-#pragma unroll 1
-  for (int g = 0; g < G; ++g) {
-    double a = -INFINITY, b = -INFINITY;                   // this lane's two largest of the group
-#pragma unroll 1
-    for (int i = 0, e = lane; e < E; ++i, e += 32) {
-      if (e / n != g) continue;
-      double v = key[i];
-      if (top2 && !bias && v > -INFINITY) v = value(e, (float)v);
-      if (v > a) { b = a; a = v; } else if (v > b) b = v;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const double c = __shfl_xor_sync(kFull, a, o), d = __shfl_xor_sync(kFull, b, o);
-      b = fmax(fmin(a, c), fmax(b, d));
-      a = fmax(a, c);
-    }
-    if (lane == g) mine = top2 && b > -INFINITY ? a + b : a;
+  for (int o = 1; o < L; o <<= 1) {
+    const double c = __shfl_xor_sync(kFull, v1, o), d = __shfl_xor_sync(kFull, v2, o);
+    v2 = fmax(fmin(v1, c), fmax(v2, d));
+    v1 = fmax(v1, c);
   }
+  const double worth = a.top2 && v2 > -INFINITY ? v1 + v2 : v1;
   int rank = 0;
-#pragma unroll 1
-  for (int g = 0; g < G; ++g) {
-    const double v = __shfl_sync(kFull, mine, g);
-    rank += v > mine || (v == mine && g < lane);
+  for (int o = 0; o < a.G; ++o) {
+    const double c = __shfl_sync(kFull, worth, o * L);
+    rank += c > worth || (c == worth && o < g);
   }
-  const unsigned keep = __ballot_sync(kFull, lane < G && rank < kept);
-  unsigned taken = 0;
+  if (rank >= a.kept) bi = -1;                             // not a kept group: nothing to give
+  unsigned long long taken = 0;
   out.idx = 0;
-#pragma unroll 1
-  for (int j = 0; j < k; ++j) {
-    double bk = -INFINITY;
-    int be = 0x7fffffff;
-#pragma unroll 1
-    for (int i = 0, e = lane; e < E; ++i, e += 32) {
-      if ((taken >> i) & 1u || !((keep >> (e / n)) & 1u)) continue;
-      if (be == 0x7fffffff || key[i] > bk) { bk = key[i]; be = e; }
-    }
+  for (int j = 0; j < a.k; ++j) {
+    double wk = bk;
+    int we = bi < 0 ? 0x7fffffff : e0 + bi * L;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-      const double c = __shfl_xor_sync(kFull, bk, o);
-      const int ce = __shfl_xor_sync(kFull, be, o);
-      if (ce != 0x7fffffff && (be == 0x7fffffff || c > bk || (c == bk && ce < be))) { bk = c; be = ce; }
+      const double c = __shfl_xor_sync(kFull, wk, o);
+      const int ce = __shfl_xor_sync(kFull, we, o);
+      if (ce != 0x7fffffff && (we == 0x7fffffff || c > wk || (c == wk && ce < we))) { wk = c; we = ce; }
     }
-    if (lane == j) out.idx = be;
-    if ((be & 31) == lane) taken |= 1u << (be >> 5);
+    if (lane == j) out.idx = we;
+    if (bi >= 0 && we == e0 + bi * L) {                    // the owner looks for its next best
+      taken |= 1ull << bi;
+      bi = -1;
+      for (int i = 0; i < count; ++i)
+        if (!((taken >> i) & 1ull) && (bi < 0 || key[i] > bk)) { bk = key[i]; bi = i; }
+    }
+  }
+  out.s = 0.0;
+  if (SCORE != MOE_SCORE_SOFTMAX && lane < a.k) {
+    const float lf = clean_logit(l[out.idx]);
+    if (lf > -INFINITY) out.s = score64((double)lf, SCORE);
   }
   return out;
+}
+
+// The rank of this lane's group by exact values, when the fp32 ones are too close at the border.
+// `near` marks the lane's experts that may be among its group's two largest (by fp32 keys less
+// twice their error); only they are evaluated in fp64.  Not for softmax (its sum is not exact).
+template <int SCORE>
+__device__ __noinline__ int exact_rank(const GroupArgs& a, const float* l, unsigned long long near, bool vec) {
+  const int lane = threadIdx.x & 31;
+  const int L = a.team, g = lane / L, tl = lane - g * L;
+  double v1 = -INFINITY, v2 = -INFINITY;
+  while (near) {
+    const int i = __ffsll((long long)near) - 1;
+    near &= near - 1;
+    const int e = g * a.n + (vec ? 4 * (tl + L * (i >> 2)) + (i & 3) : tl + L * i);
+    double v = score64((double)clean_logit(l[e]), SCORE);
+    if (a.bias) v += (double)__ldg(a.bias + e);
+    if (v > v1) { v2 = v1; v1 = v; } else if (v > v2) v2 = v;
+  }
+  __syncwarp();
+  for (int o = 1; o < L; o <<= 1) {
+    const double c = __shfl_xor_sync(kFull, v1, o), d = __shfl_xor_sync(kFull, v2, o);
+    v2 = fmax(fmin(v1, c), fmax(v2, d));
+    v1 = fmax(v1, c);
+  }
+  const double worth = a.top2 && v2 > -INFINITY ? v1 + v2 : v1;
+  int rank = 0;
+  for (int o = 0; o < a.G; ++o) {
+    const double c = __shfl_sync(kFull, worth, o * L);
+    rank += c > worth || (c == worth && o < g);
+  }
+  return rank;
 }
 
 // The v-th largest (v from 1) of the 32 lanes' values: a bitonic sort, descending by lane.
@@ -190,92 +260,131 @@ __device__ __forceinline__ float kth_of_lanes(float v, int kth) {
   return __shfl_sync(kFull, v, kth - 1);
 }
 
-struct GroupArgs {
-  const float* logits;
-  const float* bias;
-  int32_t* topk_idx;
-  float* topk_gate;
-  int T, E, k, G, n, kept, team, score, top2, renorm;
-  float scale;
-};
+// Doubles as integers of the same order (-0 as +0).
+__device__ __forceinline__ unsigned long long ordered(double v) {
+  const long long b = __double_as_longlong(v + 0.0);
+  return (unsigned long long)b ^ ((unsigned long long)(b >> 63) | 0x8000000000000000ull);
+}
 
-// EPL: keys a lane holds of its group's part; VEC: four consecutive experts per load.
-template <int EPL, bool VEC>
-__global__ void __launch_bounds__(32 * kGroupWarps)
-route_group_kernel(const GroupArgs a) {
-  extern __shared__ float gsm[];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// EPL: keys a lane can hold of its group's part, in chunks of four (VEC: four consecutive
+// experts, one load); a.chunks of them are used.
+template <int EPL, bool VEC, int SCORE>
+__global__ void __launch_bounds__(32 * kGroupWarps, EPL <= 32 ? 3 : 2)
+route_group_kernel(const __grid_constant__ GroupArgs a) {
+  extern __shared__ __align__(16) float gsm[];
+  __shared__ __align__(8) uint64_t s_bar[kGroupWarps][2];
+  __shared__ int s_abort;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int E = a.E, n = a.n, k = a.k, L = a.team;
   const int pool = a.kept * n;                             // experts of the kept groups
-  float* keys = gsm + (size_t)w * ((pool + 3) / 4 * 4);    // their fp32 keys, group by group
+  const int keys_pitch = (pool + 3) / 4 * 4;
+  float* keys = gsm + (size_t)w * (keys_pitch + (VEC ? 2 * E : 0));   // their fp32 keys, group by group
+  volatile int* abort_flag = &s_abort;
+  if (threadIdx.x == 0) s_abort = 0;
+  __syncthreads();
+  WarpRows rows;                                           // VEC: the rows of logits, one ahead
+  if (VEC) rows.init(s_bar[w], reinterpret_cast<uint8_t*>(keys + keys_pitch), (uint32_t)E * 4, lane);
   __shared__ int s_group[kGroupWarps][32];                 // the kept groups, ascending
   __shared__ int s_cand[kGroupWarps][32];
+  __shared__ double s_score[kGroupWarps][32];
   const int g = lane / L, tl = lane - g * L;               // this lane's group, its place in the team
   const bool in_g = g < a.G;
-  const bool by_logit = !a.bias && !a.top2;                // fp32 keys are exact
-  const bool need_z = a.score == MOE_SCORE_SOFTMAX && (!by_logit || !a.renorm);
+  const bool biased = a.bias != nullptr;
+  const bool by_logit = !biased && !a.top2;                // fp32 keys are exact
+  const bool need_z = SCORE == MOE_SCORE_SOFTMAX && (!by_logit || !a.renorm);
+  // expert i of the lane's part, and whether it exists (a chunk of VEC exists as a whole)
+  auto place = [&](int i) { return VEC ? 4 * (tl + L * (i >> 2)) + (i & 3) : tl + L * i; };
+  auto have = [&](int i) { return in_g && place(VEC ? i & ~3 : i) < n; };
   float bmax = 0.f;                                        // largest |bias|: part of the bound
-  if (a.bias)
-    for (int e = lane; e < E; e += 32) bmax = fmaxf(bmax, fabsf(__ldg(a.bias + e)));
+  bool odd = false;                                        // a NaN bias: every token in fp64
+  if (biased)
+    for (int e = lane; e < E; e += 32) {
+      const float b = fabsf(__ldg(a.bias + e));
+      bmax = fmaxf(bmax, b);
+      odd |= !(b < INFINITY);
+    }
   bmax = wmax(bmax);
-  const long long nw = (long long)gridDim.x * kGroupWarps;
-  for (long long t = (long long)blockIdx.x * kGroupWarps + w; t < a.T; t += nw) {
+  odd = __any_sync(kFull, odd);
+  const long long nw = (long long)gridDim.x * warps;
+  const long long first = (long long)blockIdx.x * warps + w;
+  unsigned it = 0, loaded = 0;                             // tokens done; rows asked for
+  if (VEC && lane == 0 && first < a.T) rows.load(loaded++, a.logits + first * E);
+  for (long long t = first; t < a.T; t += nw, ++it) {
     const float* l = a.logits + t * E;
     // -------------------------------------------------- logits and fp32 keys
-    float v[EPL];
-    auto place = [&](int i) { return VEC ? 4 * (tl + L * (i >> 2)) + (i & 3) : tl + L * i; };
     if constexpr (VEC) {
+      if (!rows.wait(it, abort_flag, a.err)) break;
+      l = rows.row(it);
+      __syncwarp();                                        // every lane is done with the other buffer
+      if (lane == 0 && t + nw < a.T) rows.load(loaded++, a.logits + (t + nw) * E);
+    }
+    float v[EPL];
+    auto fetch = [&](const float* p, int i, float (&f)[4], float none) {
+      if constexpr (VEC) {
+        float4 q = make_float4(none, none, none, none);
+        if (have(i)) q = *reinterpret_cast<const float4*>(p + g * n + place(i));
+        f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
+      } else {
 #pragma unroll
-      for (int i = 0; i < EPL; i += 4) {
-        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (in_g && place(i) < n) q = __ldg(reinterpret_cast<const float4*>(l + g * n + place(i)));
-        v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+        for (int c = 0; c < 4; ++c) f[c] = have(i + c) ? __ldg(p + g * n + place(i + c)) : none;
       }
-    } else {
+    };
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) v[i] = in_g && place(i) < n ? __ldg(l + g * n + place(i)) : -INFINITY;
+    for (int i = 0; i < EPL; i += 4) {
+      float f[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (i < 4 * a.chunks) fetch(l, i, f, -INFINITY);     // uniform
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[i + c] = f[c];
     }
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) v[i] = clean_logit(v[i]);
+    for (int i = 0; i < EPL; ++i)
+      if ((i & ~3) < 4 * a.chunks) v[i] = clean_logit(v[i]);
     float m = -INFINITY, z = 0.f, delta = 0.f;
-    if (need_z) {
+    if (need_z || !by_logit) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) m = fmaxf(m, v[i]);
+      for (int i = 0; i < EPL; ++i)
+        if ((i & ~3) < 4 * a.chunks) m = fmaxf(m, v[i]);
       m = wmax(m);
-      if (m > -INFINITY) {
+    }
+    if (need_z && m > -INFINITY) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) z += expf(v[i] - m);
-        z = wsum(z);
-      }
+      for (int i = 0; i < EPL; ++i)
+        if ((i & ~3) < 4 * a.chunks) z += expf(v[i] - m);
+      z = wsum(z);
     }
     const bool dead = need_z && !(m > -INFINITY);          // every expert masked
+    bool slow = odd;
     if (!by_logit) {
-      float smax = 0.f;
       const float iz = __fdividef(1.f, z);
+      auto score_of = [&](float x, float y) {
+        if (SCORE == MOE_SCORE_SOFTMAX) return make_float2(__expf(x - m) * iz, __expf(y - m) * iz);
+        return score32<SCORE>(x, y);
+      };
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        if (v[i] > -INFINITY) {
-          const float s = a.score == MOE_SCORE_SOFTMAX ? __expf(v[i] - m) * iz : score32(v[i], a.score);
-          smax = fmaxf(smax, s);
-          if (a.bias) {
-            const float b = s + __ldg(a.bias + g * n + place(i));
-            v[i] = b == b ? b : -INFINITY;
-          } else {
-            v[i] = s;
-          }
+      for (int i = 0; i < EPL; i += 4) {
+        if (i >= 4 * a.chunks) continue;                   // uniform
+        float b[4] = {0.f, 0.f, 0.f, 0.f};
+        if (biased) fetch(a.bias, i, b, 0.f);
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          const float2 s = score_of(v[i + c], v[i + c + 1]);
+          const float2 key = unpack2(add2(pack2(s.x, s.y), pack2(b[c], b[c + 1])));
+          v[i + c] = v[i + c] > -INFINITY ? key.x : -INFINITY;
+          v[i + c + 1] = v[i + c + 1] > -INFINITY ? key.y : -INFINITY;
         }
       }
-      // the scores' error (see score32; where even the largest score is small, its logit is
-      // about 2 log of it; softmax: the sum and its reciprocal instead), one rounding of s + b
-      smax = wmax(smax);
-      const float rel =
-          a.score == MOE_SCORE_SOFTMAX ? 3e-6f : 2e-6f + 4.8e-7f * fmaxf(0.f, -__logf(fmaxf(smax, 1e-37f)));
+      // the scores' error relative to the largest one, the largest logit's (see score32; softmax:
+      // the sum and its reciprocal instead), and one rounding of s + b
+      const float smax = dead ? 0.f : score_of(m, m).x;
+      const float rel = SCORE == MOE_SCORE_SOFTMAX ? 3e-6f : 2e-6f + 2.4e-7f * fmaxf(0.f, -m);
       delta = rel * smax + 2.4e-7f * bmax;
+      slow |= !(smax > 1e-12f);                            // near the flushed subnormals
     }
     // -------------------------------------------------- groups
     float g1 = -INFINITY, g2 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
+      if ((i & ~3) >= 4 * a.chunks) continue;
       g2 = fmaxf(g2, fminf(g1, v[i]));
       g1 = fmaxf(g1, v[i]);
     }
@@ -284,44 +393,61 @@ route_group_kernel(const GroupArgs a) {
       g2 = fmaxf(fminf(g1, c1), fmaxf(g2, c2));
       g1 = fmaxf(g1, c1);
     }
-    const float gv = a.top2 && g2 > -INFINITY ? g1 + g2 : g1;
-    int rank = 0;
-    bool slow = false;
-    for (int o = 0; o < a.G; ++o) {
-      const float c = __shfl_sync(kFull, gv, o * L);
-      rank += c > gv || (c == gv && o < g);
-    }
-    const bool keep = in_g && rank < a.kept;
-    if (!by_logit && a.kept < a.G) {                       // the border must be wider than the error
-      const float lo = wmax(keep ? -gv : -INFINITY), hi = wmax(in_g && !keep ? gv : -INFINITY);
-      slow = !(-lo - hi > 6.f * delta + 2.4e-7f * (fabsf(lo) + fabsf(hi))) && hi > -INFINITY;
+    bool keep = in_g;
+    if (a.kept < a.G) {
+      const float gv = a.top2 && g2 > -INFINITY ? g1 + g2 : g1;
+      int rank = 0;
+      for (int o = 0; o < a.G; ++o) {
+        const float c = __shfl_sync(kFull, gv, o * L);
+        rank += c > gv || (c == gv && o < g);
+      }
+      keep = in_g && rank < a.kept;
+      if (!by_logit) {                                     // the border must be wider than the error
+        const float lo = wmax(keep ? -gv : -INFINITY), hi = wmax(in_g && !keep ? gv : -INFINITY);
+        if (!(-lo - hi > 6.f * delta + 2.4e-7f * (fabsf(lo) + fabsf(hi))) && hi > -INFINITY) {
+          if (SCORE == MOE_SCORE_SOFTMAX) {
+            slow = true;
+          } else {
+            const float th = (a.top2 ? g2 : g1) - 2.f * delta;
+            unsigned long long near = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+              if (v[i] > -INFINITY && v[i] >= th) near |= 1ull << i;
+            keep = exact_rank<SCORE>(a, l, near, VEC) < a.kept && in_g;
+          }
+        }
+      }
     }
     const unsigned heads = __ballot_sync(kFull, keep && tl == 0);
     const int order = __popc(heads & ((1u << (g * L)) - 1u));   // this group's place among the kept
     // -------------------------------------------------- the kept groups' keys, spread evenly
-    if (a.top2 && !a.bias) {
-      // groups by scores, experts by logit: the logits again
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (keep && place(i) < n) v[i] = clean_logit(__ldg(l + g * n + place(i)));
-      delta = 0.f;
-    }
+    const bool again = a.top2 && !biased;                  // groups by scores, experts by logit
+    if (again) delta = 0.f;
     __syncwarp();                                          // the previous token's keys are read
     if (keep) {
       if (tl == 0) s_group[w][order] = g;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (place(i) < n) keys[order * n + place(i)] = v[i];
+      for (int i = 0; i < EPL; i += 4) {
+        if (i >= 4 * a.chunks) continue;
+        float f[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+        if (again) {
+          fetch(l, i, f, -INFINITY);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) f[c] = clean_logit(f[c]);
+        }
+        if constexpr (VEC) {
+          if (have(i)) *reinterpret_cast<float4*>(keys + order * n + place(i)) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (have(i + c)) keys[order * n + place(i + c)] = f[c];
+        }
+      }
     }
     __syncwarp();
     float best = -INFINITY;
     for (int p = lane; p < pool; p += 32) best = fmaxf(best, keys[p]);
     float tau = kth_of_lanes(best, k);
-    auto count = [&](float th) {
-      int c = 0;
-      for (int p = lane; p < pool; p += 32) c += keys[p] >= th;
-      return (int)__reduce_add_sync(kFull, (unsigned)c);
-    };
     // the keys not below the threshold, in index order; the first 32 get a lane each
     auto compact = [&]() {
       const float th = tau - 2.f * delta - (delta > 0.f ? 2.4e-7f * fabsf(tau) : 0.f);
@@ -343,7 +469,9 @@ route_group_kernel(const GroupArgs a) {
       float lo = tau, hi = wmax(best);
       for (int it = 0; it < 24; ++it) {
         const float mid = 0.5f * lo + 0.5f * hi;
-        const int above = count(mid);
+        int above = 0;
+        for (int p = lane; p < pool; p += 32) above += keys[p] >= mid;
+        above = (int)__reduce_add_sync(kFull, (unsigned)above);
         if (above >= k) lo = mid; else hi = mid;
         if (above >= k && above <= 32) break;
       }
@@ -358,69 +486,102 @@ route_group_kernel(const GroupArgs a) {
     pick.idx = 0;
     pick.m = (double)m;
     pick.z = (double)z;
+    pick.s = 0.0;
     if (!slow) {
       int e = 0;
-      double key = -INFINITY;
+      double key = -INFINITY, s = 0.0;
+      float af = 0.f;
       if (lane < c) {
         const int p = s_cand[w][lane];
         const int o = p / n;
         e = s_group[w][o] * n + (p - o * n);
-        if (!a.bias)
-          key = (double)clean_logit(__ldg(l + e));
-        else if (a.score == MOE_SCORE_SOFTMAX)
-          key = (double)keys[p];                           // checked against delta below
-        else
-          key = score64((double)clean_logit(__ldg(l + e)), a.score) + (double)__ldg(a.bias + e);
+        af = keys[p];
+        const double lf = (double)clean_logit(l[e]);
+        if (SCORE != MOE_SCORE_SOFTMAX) s = score64(lf, SCORE);
+        key = !biased ? lf : SCORE == MOE_SCORE_SOFTMAX ? (double)af : s + (double)__ldg(a.bias + e);
       }
+      // rank = how many are larger; of equal ones the lower lane (index) goes first, so a lower
+      // lane counts from equal on.  The upper halves of the ordered keys decide, unless two lanes
+      // have the same one.
+      const unsigned long long ok = ordered(key);
+      const unsigned hi = (unsigned)(ok >> 32);
+      const unsigned same = __match_any_sync(kFull, lane < c ? hi : 0u);   // a key's half is never 0
       int r = 0;
-      bool near = false;
-      const double gap = a.bias && a.score == MOE_SCORE_SOFTMAX ? 2.0 * (double)delta : -1.0;
-      for (int j = 0; j < c; ++j) {
-        const double o = __shfl_sync(kFull, key, j);
-        // candidates are in index order, so a lower lane is a lower index
-        r += o > key || (o == key && j < lane);
-        near = near || (j != lane && fabs(o - key) <= gap);
-      }
-      slow = __any_sync(kFull, near && lane < c);
-      if (lane < c && r < k) s_cand[w][r] = e;             // every lane has read its candidate
-      __syncwarp();
-      if (lane < k) pick.idx = s_cand[w][lane];
-    }
-    if (slow) pick = route_token_fp64(l, a.bias, E, n, a.G, a.kept, k, a.score, a.top2);
-    // -------------------------------------------------- gates (fp64, rounded once)
-    const bool act = lane < k;
-    const float lf = act ? clean_logit(__ldg(l + pick.idx)) : -INFINITY;
-    double s = 0.0;
-    if (a.score == MOE_SCORE_SOFTMAX) {
-      if (a.renorm) {
-        const double mm = wmax_d((double)lf);
-        s = lf > -INFINITY ? exp((double)lf - mm) : 0.0;
+      if (__all_sync(kFull, lane >= c || same == 1u << lane)) {
+        for (int j = 0; j < c; ++j) r += __shfl_sync(kFull, hi, j) > hi;
       } else {
-        s = lf > -INFINITY && !dead ? exp((double)lf - pick.m) / pick.z : 0.0;
+        for (int j = 0; j < c; ++j) r += __shfl_sync(kFull, ok, j) > ok - (j < lane ? 1 : 0);
       }
-    } else if (lf > -INFINITY) {
-      s = score64((double)lf, a.score);
+      if (SCORE == MOE_SCORE_SOFTMAX && biased) {
+        // these keys are fp32: two within their error are decided in fp64
+        bool near = false;
+        for (int j = 0; j < c; ++j) {
+          const float o = __shfl_sync(kFull, af, j);       // by every lane, whatever it has found
+          near |= fabsf(o - af) <= 2.f * delta && j != lane;
+        }
+        slow = __any_sync(kFull, near && lane < c);
+      }
+      if (lane < c && r < k) {                             // every lane has read its candidate
+        s_cand[w][r] = e;
+        s_score[w][r] = s;
+      }
+      __syncwarp();
+      if (lane < k) {
+        pick.idx = s_cand[w][lane];
+        pick.s = s_score[w][lane];
+      }
+    }
+    if (slow) pick = route_token_fp64<SCORE>(a, l);
+    // -------------------------------------------------- gates (fp64, rounded once)
+    double s = 0.0;
+    if (SCORE == MOE_SCORE_SOFTMAX) {
+      const float lf = lane < k ? clean_logit(l[pick.idx]) : -INFINITY;
+      const double mm = a.renorm ? (double)wmax(lf) : pick.m;
+      if (lf > -INFINITY) s = exp((double)lf - mm);
+      if (!a.renorm) s /= pick.z;
+    } else if (lane < k) {
+      s = pick.s;
     }
     if (a.renorm) {
       const double tot = wsum_d(s);
       s = tot > 0.0 ? s / tot : 0.0;
     }
-    if (act) {
+    if (lane < k) {
       a.topk_idx[t * k + lane] = pick.idx;
       a.topk_gate[t * k + lane] = (float)(s * (double)a.scale);
     }
-    __syncwarp();
   }
+  if (VEC && lane == 0) rows.drain(it, loaded, a.err);     // after a timeout: what is still in flight
 }
 
-template <int EPL, bool VEC>
+// Warps a block: eight, or fewer where the tokens would leave multiprocessors without any.
+template <int EPL, bool VEC, int SCORE>
 moe_status run_group(const GroupArgs& a, cudaStream_t s) {
-  const size_t smem = (size_t)kGroupWarps * ((a.kept * a.n + 3) / 4 * 4) * sizeof(float);   // at most 32 KB
-  long long blocks = ((long long)a.T + kGroupWarps - 1) / kGroupWarps;
-  const long long cap = (long long)num_sms() * 8;
+  const int sms = num_sms();
+  int warps = (a.T + sms - 1) / sms;
+  if (warps > kGroupWarps) warps = kGroupWarps;
+  constexpr size_t kMost = (size_t)kGroupWarps * 3 * 4096; // three rows of 1024 a warp
+  static std::atomic<int> configured[kMaxDevices];
+  const moe_status st = ensure_smem_limit(configured, route_group_kernel<EPL, VEC, SCORE>, kMost);
+  if (st != MOE_OK) return st;
+  const size_t smem = (size_t)warps * ((a.kept * a.n + 3) / 4 * 4 + (VEC ? 2 * a.E : 0)) * sizeof(float);
+  long long blocks = ((long long)a.T + warps - 1) / warps;
+  const long long cap = (long long)sms * 3;
   if (blocks > cap) blocks = cap;
-  route_group_kernel<EPL, VEC><<<(unsigned)blocks, 32 * kGroupWarps, smem, s>>>(a);
+  route_group_kernel<EPL, VEC, SCORE><<<(unsigned)blocks, 32 * warps, smem, s>>>(a);
   return check_launch();
+}
+
+template <int SCORE>
+moe_status dispatch_group(const GroupArgs& a, bool vec, cudaStream_t s) {
+  if (vec) {
+    if (a.chunks <= 2) return run_group<8, true, SCORE>(a, s);
+    if (a.chunks <= 8) return run_group<32, true, SCORE>(a, s);
+    return run_group<64, true, SCORE>(a, s);
+  }
+  if (a.chunks <= 2) return run_group<8, false, SCORE>(a, s);
+  if (a.chunks <= 8) return run_group<32, false, SCORE>(a, s);
+  return run_group<64, false, SCORE>(a, s);
 }
 
 }  // namespace
@@ -428,25 +589,16 @@ moe_status run_group(const GroupArgs& a, cudaStream_t s) {
 moe_status launch_route_grouped(const float* logits, int T, int E, int k, int n_groups, int groups_kept,
                                 int group_score, int score, int renorm, float scale, const float* bias,
                                 int32_t* topk_idx, float* topk_gate, cudaStream_t s) {
-  GroupArgs a{logits, bias, topk_idx, topk_gate, T, E, k, n_groups, E / n_groups, groups_kept, 0, score,
-              group_score == MOE_GROUP_TOP2, renorm, scale};
+  GroupArgs a{logits, bias, topk_idx, topk_gate, T, E, k, n_groups, E / n_groups, groups_kept, 0, 0,
+              group_score == MOE_GROUP_TOP2, renorm, scale, err_ptr()};
   int p2 = 1;
   while (p2 < n_groups) p2 <<= 1;
   a.team = 32 / p2;
-  const bool vec = a.n % 4 == 0 && aligned16(logits);
-  const int per = vec ? (a.n / 4 + a.team - 1) / a.team * 4 : (a.n + a.team - 1) / a.team;   // at most 64
-  if (vec) {
-    if (per <= 4) return run_group<4, true>(a, s);
-    if (per <= 8) return run_group<8, true>(a, s);
-    if (per <= 16) return run_group<16, true>(a, s);
-    if (per <= 32) return run_group<32, true>(a, s);
-    return run_group<64, true>(a, s);
-  }
-  if (per <= 4) return run_group<4, false>(a, s);
-  if (per <= 8) return run_group<8, false>(a, s);
-  if (per <= 16) return run_group<16, false>(a, s);
-  if (per <= 32) return run_group<32, false>(a, s);
-  return run_group<64, false>(a, s);
+  const bool vec = a.n % 4 == 0 && aligned16(logits) && aligned16(bias);
+  a.chunks = (a.n + 4 * a.team - 1) / (4 * a.team);        // at most 16: n <= 1024 / G, G > p2 / 2
+  if (score == MOE_SCORE_SOFTMAX) return dispatch_group<MOE_SCORE_SOFTMAX>(a, vec, s);
+  if (score == MOE_SCORE_SIGMOID) return dispatch_group<MOE_SCORE_SIGMOID>(a, vec, s);
+  return dispatch_group<MOE_SCORE_SQRT_SOFTPLUS>(a, vec, s);
 }
 
 }  // namespace moe

@@ -112,7 +112,7 @@ _SIGNATURES = {
     "moe_combine_norm": (_i32, [_c_void_p, _i32, _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _i32, _i64,
                                 _c_void_p, _c_void_p, _i32, _f32, _c_void_p, _f32, _i32, _i32, _c_void_p, _c_void_p,
                                 _c_void_p, _i32, _c_void_p]),
-    "moe_block_norm_backward_workspace_bytes": (_size, [_i32, _i32, _i32]),
+    "moe_block_norm_backward_workspace_bytes": (_size, [_i32, _i32]),
     "moe_block_norm_backward": (_i32, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32, _i32, _i32, _c_void_p,
                                        _c_void_p, _i32, _f32, _c_void_p, _f32, _i32, _i32, _c_void_p, _c_void_p,
                                        _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p]),
@@ -695,18 +695,20 @@ class _on:
         self.back = torch.cuda.current_device()
         if self.back != self.index:
             torch.cuda.set_device(self.index)
+        return self
 
     def __exit__(self, *exc):
         if self.back != self.index:
             torch.cuda.set_device(self.back)
 
+    def stream(self, given):
+        """The given stream's handle, or the current one's (read without building a Stream object,
+        which costs 3 us of a small call's 15)."""
+        return torch._C._cuda_getCurrentRawStream(self.index) if given is None else given.cuda_stream
+
 
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
-
-
-def _cuda_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def _rows_of(t: torch.Tensor, name: str, rows: int, cols=None, dtype=None):
@@ -738,11 +740,11 @@ def moe_route_grouped(logits, k: int, n_groups: int, groups_kept: int, group_sco
         _need(topk_idx, "topk_idx", torch.int32, (T, k))
     topk_gate = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_gate is None else \
         _need(topk_gate, "topk_gate", torch.float32, (T, k))
-    with _on(logits, select_bias, topk_idx, topk_gate):
+    with _on(logits, select_bias, topk_idx, topk_gate) as on:
         _check("moe_route_grouped", lib().moe_route_grouped(
             _ptr(logits), _ptr(select_bias), T, E, k, n_groups, groups_kept,
             _choice(GROUP_SCORE, group_score, "group_score"), _choice(SCORE, score, "score"), 1 if renormalize else 0,
-            scale, _ptr(topk_idx), _ptr(topk_gate), _cuda_stream(stream)))
+            scale, _ptr(topk_idx), _ptr(topk_gate), on.stream(stream)))
     return topk_idx, topk_gate
 
 
@@ -764,10 +766,10 @@ def moe_route_backward(logits, topk_idx=None, d_gate=None, score: str = "softmax
     if load is not None:
         _need(load, "load", torch.float32, (E,))
     d_logits = torch.empty_like(logits) if d_logits is None else _need(d_logits, "d_logits", torch.float32, (T, E))
-    with _on(logits, topk_idx, d_gate, load, d_logits):
+    with _on(logits, topk_idx, d_gate, load, d_logits) as on:
         _check("moe_route_backward", lib().moe_route_backward(
             _ptr(logits), _ptr(topk_idx), _ptr(d_gate), T, E, k, _choice(SCORE, score, "score"),
-            1 if renormalize else 0, scale, _ptr(load), aux_coef, z_coef, _ptr(d_logits), _cuda_stream(stream)))
+            1 if renormalize else 0, scale, _ptr(load), aux_coef, z_coef, _ptr(d_logits), on.stream(stream)))
     return d_logits
 
 
@@ -786,9 +788,9 @@ def moe_quantize_rows_i8(x, row_of=None, rows_max: int = 0, q=None, scale=None, 
         _rows_of(q, "q", out, cols, torch.int8)
     scale = torch.empty((out,), dtype=torch.float32, device=x.device) if scale is None else \
         _rows_of(scale, "scale", out, None, torch.float32)
-    with _on(x, row_of, q, scale):
+    with _on(x, row_of, q, scale) as on:
         _check("moe_quantize_rows_i8", lib().moe_quantize_rows_i8(
-            _ptr(x), _dt(x), rows, cols, _ptr(row_of), k, out, _ptr(q), _ptr(scale), _cuda_stream(stream)))
+            _ptr(x), _dt(x), rows, cols, _ptr(row_of), k, out, _ptr(q), _ptr(scale), on.stream(stream)))
     return q, scale
 
 
@@ -816,16 +818,16 @@ def moe_expert_gate_up_i8(x_q, x_scale, offsets, W_gu, w_scale, rows_max: int, h
     _rows_of(x_scale, "x_scale", rows, None, torch.float32)
     h = torch.empty((rows_max, F), dtype=torch.bfloat16, device=x_q.device) if h is None else \
         _rows_of(h, "h", rows_max, F, torch.bfloat16)
-    with _on(x_q, x_scale, offsets, W_gu, w_scale, h, token_of_row):
+    with _on(x_q, x_scale, offsets, W_gu, w_scale, h, token_of_row) as on:
         if token_of_row is None:
             _check("moe_expert_gate_up_i8", lib().moe_expert_gate_up_i8(
                 _ptr(x_q), _ptr(x_scale), _ptr(offsets), E, d, F, rows_max, _ptr(W_gu), _ptr(w_scale), _ptr(h),
-                _cuda_stream(stream)))
+                on.stream(stream)))
         else:
             _rows_of(token_of_row, "token_of_row", rows_max, None, torch.int32)
             _check("moe_expert_gate_up_gather_i8", lib().moe_expert_gate_up_gather_i8(
                 _ptr(x_q), _ptr(x_scale), T, _ptr(token_of_row), _ptr(offsets), E, d, F, rows_max, _ptr(W_gu),
-                _ptr(w_scale), _ptr(h), _cuda_stream(stream)))
+                _ptr(w_scale), _ptr(h), on.stream(stream)))
     return h
 
 
@@ -843,10 +845,10 @@ def moe_expert_down_i8(h_q, h_scale, offsets, W_dn, w_scale, rows_max: int, gate
         _rows_of(gate_of_row, "gate_of_row", rows_max, None, torch.float32)
     y_rows = torch.empty((rows_max, d), dtype=y_dtype or torch.float32, device=h_q.device) if y_rows is None else \
         _rows_of(y_rows, "y_rows", rows_max, d, y_dtype)
-    with _on(h_q, h_scale, offsets, W_dn, w_scale, gate_of_row, y_rows):
+    with _on(h_q, h_scale, offsets, W_dn, w_scale, gate_of_row, y_rows) as on:
         _check("moe_expert_down_i8", lib().moe_expert_down_i8(
             _ptr(h_q), _ptr(h_scale), _ptr(offsets), E, d, F, rows_max, _ptr(W_dn), _ptr(w_scale), _ptr(gate_of_row),
-            _dt(y_rows), _ptr(y_rows), _cuda_stream(stream)))
+            _dt(y_rows), _ptr(y_rows), on.stream(stream)))
     return y_rows
 
 
@@ -887,11 +889,11 @@ def moe_block_norm(residual, y=None, post_weight=None, gate=None, alpha: float =
     G = _norm_params(d, post_weight, gate, pre_weight)
     x_out, n_out = _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, y is not None)
     rt = _dt(residual)
-    with _on(residual, y, post_weight, gate, pre_weight, x_out, n_out):
+    with _on(residual, y, post_weight, gate, pre_weight, x_out, n_out) as on:
         _check("moe_block_norm", lib().moe_block_norm(
             _ptr(residual), rt, _ptr(y), rt if y is None else _dt(y), _ptr(post_weight), _ptr(gate), G, alpha,
             _ptr(pre_weight), eps, T, d, _ptr(x_out), _ptr(n_out), rt if n_out is None else _dt(n_out),
-            _cuda_stream(stream)))
+            on.stream(stream)))
     return x_out, n_out
 
 
@@ -914,11 +916,11 @@ def moe_combine_norm(residual, y_rows, row_of, rows_max: int, topk_gate=None, sh
     G = _norm_params(d, post_weight, gate, pre_weight)
     x_out, n_out = _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, True)
     rt = _dt(residual)
-    with _on(residual, y_rows, row_of, topk_gate, shared_y, post_weight, gate, pre_weight, y_out, x_out, n_out):
+    with _on(residual, y_rows, row_of, topk_gate, shared_y, post_weight, gate, pre_weight, y_out, x_out, n_out) as on:
         _check("moe_combine_norm", lib().moe_combine_norm(
             _ptr(residual), rt, _ptr(y_rows), _dt(y_rows), _ptr(row_of), _ptr(topk_gate), _ptr(shared_y), k, rows_max,
             _ptr(post_weight), _ptr(gate), G, alpha, _ptr(pre_weight), eps, T, d, _ptr(y_out), _ptr(x_out),
-            _ptr(n_out), rt if n_out is None else _dt(n_out), _cuda_stream(stream)))
+            _ptr(n_out), rt if n_out is None else _dt(n_out), on.stream(stream)))
     return x_out, n_out
 
 
@@ -951,13 +953,13 @@ def moe_block_norm_backward(d_x, d_n, x_out, y=None, post_weight=None, gate=None
     d_pre_weight = out(d_pre_weight, "d_pre_weight", pre_weight, f32)
     rt = _dt(x_out)
     with _on(x_out, d_x, d_n, y, post_weight, gate, pre_weight, d_residual, d_y, d_post_weight, d_gate, d_pre_weight,
-             workspace):
-        nb = lib().moe_block_norm_backward_workspace_bytes(T, d, G)
+             workspace) as on:
+        nb = lib().moe_block_norm_backward_workspace_bytes(T, d)
         ws = _ws(nb, dev, workspace)
         _check("moe_block_norm_backward", lib().moe_block_norm_backward(
             _ptr(d_x), _ptr(d_n), _ptr(x_out), _ptr(y), rt, rt if d_n is None else _dt(d_n), rt if y is None else _dt(y),
             _ptr(post_weight), _ptr(gate), G, alpha, _ptr(pre_weight), eps, T, d, _ptr(d_residual), _ptr(d_y),
-            _ptr(d_post_weight), _ptr(d_gate), _ptr(d_pre_weight), _ptr(ws), nb, _cuda_stream(stream)))
+            _ptr(d_post_weight), _ptr(d_gate), _ptr(d_pre_weight), _ptr(ws), nb, on.stream(stream)))
     return {"d_residual": d_residual, "d_y": d_y, "d_post_weight": d_post_weight, "d_gate": d_gate,
             "d_pre_weight": d_pre_weight}
 
