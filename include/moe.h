@@ -778,7 +778,6 @@ MOE_API moe_status moe_route_backward(const float* logits, const int32_t* topk_i
  *   x_q      (device) [rows_max, d] int8;  x_scale (device) [rows_max] fp32
  *   W_gu     (device) [E, 2F, d] int8 (gate rows, then up rows);  w_scale (device) [E, 2F] fp32
  *   h        (device) [rows_max, F] bf16 out
- *   Tile orientation as moe_gate_up_weight_major says.
  * moe_expert_gate_up_gather_i8 -- the same rows read through token_of_row from x_q [T, d] and
  *   x_scale [T] (weight-major tiles, whatever the group sizes).  A token index outside [0, T)
  *   is recorded as MOE_DEVERR_ROW and row 0 is read in its place.
@@ -790,6 +789,7 @@ MOE_API moe_status moe_route_backward(const float* logits, const int32_t* topk_i
  * Errors: INVALID_ARG for a null pointer (gate_of_row may be), a negative size or a bad
  * y_dtype; UNSUPPORTED for E > 1024, d or F not a multiple of 16 or outside [128, 16384],
  * rows_max >= 2^31, an unaligned pointer, or a driver that encodes no tensor maps.
+ * Tile orientation of both GEMMs as moe_gate_up_weight_major says.
  * ---------------------------------------------------------------------------------- */
 MOE_API moe_status moe_quantize_rows_i8(const void* x, int32_t x_dtype, int64_t rows, int32_t cols,
                      const int32_t* row_of, int32_t k, int64_t rows_max, int8_t* q, float* scale,

@@ -110,25 +110,16 @@ __device__ __forceinline__ void stage_red32(uint8_t* stage, const float (&v)[32]
   __syncwarp();
 }
 
-// Four column scales from column col of n (a multiple of 16, as col is of 4); 0 past the end.
-// Every lane reads the same address.
-__device__ __forceinline__ void col_scale4(const float* __restrict__ w, int col, int n, float (&f)[4]) {
-  const float4 q = col < n ? __ldg(reinterpret_cast<const float4*>(w + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
-  f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
-}
-// 32 accumulators of a row times the row's factor (I8: and their column scales).
+// 32 accumulators of a row times the row's factor.  I8: and the column scales, read four at a
+// time from shared memory, the same address for every lane.
 template <bool I8>
-__device__ __forceinline__ void scaled32(const uint32_t (&v)[32], float gs, const float* __restrict__ w_scale, int col,
-                                         int n, float (&y)[32]) {
+__device__ __forceinline__ void scaled32(const uint32_t (&v)[32], float gs, const float* col_scale, float (&y)[32]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    if constexpr (I8) {
-      float s[4];
-      col_scale4(w_scale, col + (i & ~3), n, s);
-      y[i] = acc_value<true>(v[i]) * gs * s[i & 3];
-    } else {
-      y[i] = __uint_as_float(v[i]) * gs;
-    }
+  for (int i = 0; i < 32; i += 4) {
+    const float4 s = I8 ? *reinterpret_cast<const float4*>(col_scale + i) : make_float4(1.f, 1.f, 1.f, 1.f);
+    const float f[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[i + c] = I8 ? acc_value<true>(v[i + c]) * gs * f[c] : __uint_as_float(v[i + c]) * gs;
   }
 }
 
@@ -139,15 +130,16 @@ __device__ __forceinline__ void scaled32(const uint32_t (&v)[32], float gs, cons
 // .sync.aligned); rows past wrows are read but not stored.
 //   MODE 0: columns [0,128) gate, [128,256) up -> H = silu(g) * u for features n_tile*128 + ...
 //   MODE 1: 256 columns -> gate_of_row[row] * acc for outputs n_tile*256 + ...
-// MODE 1 / 3 process the 32-column chunks [c_begin, c_end) of the 256 (a warp may own half).
+// The chunks [c_begin, c_end) of the 256 columns' eight (a warp may own half; MODE 0: half of the
+// 128 features).
 // I8: the accumulators are int32 sums of 8-bit products; gs carries the row's scale (times its
-// gate in MODE 1), and w_scale points to the expert's column scales (gate columns, then up).
+// gate in MODE 1), and col_scale (shared memory) the scales of the tile's 256 weight rows.
 template <int MODE, typename OutT, bool I8 = false>
 __device__ __forceinline__ void epilogue_tile(uint32_t taddr, uint8_t* stage, int lane, long long wrow0, int wrows,
                                               int n_tile, int F, int N_out, const float* __restrict__ gate_of_row,
                                               OutT* __restrict__ out, const int32_t* __restrict__ token_of_row,
                                               int n_tokens, int* err, float gs, int c_begin = 0,
-                                              int c_end = BN / 32, const float* __restrict__ w_scale = nullptr) {
+                                              int c_end = BN / 32, const float* col_scale = nullptr) {
   if constexpr (MODE == 3) {
     const int n0 = n_tile * BN;
     const uint64_t pol = l2_evict_last_policy();
@@ -173,27 +165,22 @@ __device__ __forceinline__ void epilogue_tile(uint32_t taddr, uint8_t* stage, in
   } else if constexpr (MODE == 0 || MODE == 4) {
     const int f0 = n_tile * 128;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = c_begin / 2; c < c_end / 2; ++c) {
       uint32_t g[32], u[32];
       tmem_ld32(taddr + c * 32, g);
       tmem_ld32(taddr + 128 + c * 32, u);
       tmem_wait_ld();
       tmem_regs_ready(g);
       tmem_regs_ready(u);
-      float h[32];
+      float h[32], gf[32], uf[32];
+      // the factor of bf16 accumulators is 1: theirs are taken as they are
+      if constexpr (I8) {
+        scaled32<true>(g, gs, col_scale + c * 32, gf);
+        scaled32<true>(u, gs, col_scale + 128 + c * 32, uf);
+      }
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        float gi, ui;
-        if constexpr (I8) {
-          float sg[4], su[4];
-          col_scale4(w_scale, f0 + c * 32 + (i & ~3), F, sg);
-          col_scale4(w_scale + F, f0 + c * 32 + (i & ~3), F, su);
-          gi = acc_value<true>(g[i]) * (gs * sg[i & 3]);
-          ui = acc_value<true>(u[i]) * (gs * su[i & 3]);
-        } else {
-          gi = __uint_as_float(g[i]);
-          ui = __uint_as_float(u[i]);
-        }
+        const float gi = I8 ? gf[i] : __uint_as_float(g[i]), ui = I8 ? uf[i] : __uint_as_float(u[i]);
         // fast exp / divide: H is rounded to bf16 next, far coarser than their error; the
         // exact forms made this epilogue the bound of the gate/up GEMM
         h[i] = __fdividef(gi, 1.f + __expf(-gi)) * ui;
@@ -215,10 +202,10 @@ __device__ __forceinline__ void epilogue_tile(uint32_t taddr, uint8_t* stage, in
       tmem_regs_ready(va);
       tmem_regs_ready(vb);
       float y[32];
-      scaled32<I8>(va, gs, w_scale, n0 + c * 32, N_out, y);
+      scaled32<I8>(va, gs, col_scale + c * 32, y);
       stage_store32<OutT>(stage, y, lane, out, wrow0, wrows, N_out, n0 + c * 32, N_out);
       if (two) {
-        scaled32<I8>(vb, gs, w_scale, n0 + (c + 1) * 32, N_out, y);
+        scaled32<I8>(vb, gs, col_scale + (c + 1) * 32, y);
         stage_store32<OutT>(stage, y, lane, out, wrow0, wrows, N_out, n0 + (c + 1) * 32, N_out);
       }
     }
@@ -303,14 +290,13 @@ __device__ __forceinline__ void gather_producer(const CUtensorMap* tmB, uint32_t
   }
 }
 
-template <int MODE, typename OutT, bool I8 = false>
+template <int MODE, typename OutT>
 __global__ void __launch_bounds__(kThreadsTC, 1)
 grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const int32_t* __restrict__ offsets, int E, int K, int N_out, int F,
                        long long rows_max, const float* __restrict__ gate_of_row,
                        OutT* __restrict__ out, const int32_t* __restrict__ token_of_row, int n_tokens,
-                       const __nv_bfloat16* __restrict__ a_gather, int* err, const float* __restrict__ row_scale,
-                       const float* __restrict__ w_scale) {
+                       const __nv_bfloat16* __restrict__ a_gather, int* err) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -416,7 +402,8 @@ grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
           const uint64_t bdesc = sw128_desc(sb + L::b + stage * B_STAGE);
 #pragma unroll
           for (int kk = 0; kk < BK / UMMA_K; ++kk)   // +32 bytes along K per step (>> 4 = 2)
-            umma<I8>(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, make_idesc_of<I8>(BM, BN), (kb | kk) != 0 ? 1u : 0u);
+            umma_bf16(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, make_idesc(BM, BN),
+                      (kb | kk) != 0 ? 1u : 0u);
           umma_commit(bar_empty + 8 * stage);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -440,9 +427,8 @@ grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
       const long long wrow0 = (long long)tc.row0 + q * 32;          // first row of this warp
       const int wrows = min(32, max(0, tc.rows - q * 32));          // valid rows of this warp
       // the row's gate, fetched while the tile's MMAs still run
-      float gs = ((MODE == 1 || MODE == 3) && lane < wrows && gate_of_row) ? __ldg(gate_of_row + wrow0 + lane) : 1.f;
-      if (I8) gs *= lane < wrows ? __ldg(row_scale + wrow0 + lane) : 0.f;
-      const float* ws = I8 ? w_scale + (long long)tc.e * (MODE == 0 ? 2 * F : N_out) : nullptr;
+      const float gs = ((MODE == 1 || MODE == 3) && lane < wrows && gate_of_row) ? __ldg(gate_of_row + wrow0 + lane)
+                                                                                  : 1.f;
       const bool got = mbar_wait(bar_tfull + 8 * acc, acc_phase, abort_flag, err);
       // tcgen05.ld is .sync.aligned: the whole warp goes on, or the whole warp stops
       if (!__all_sync(0xffffffffu, got)) break;
@@ -452,8 +438,8 @@ grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
       (void)r_in;
       // a warp past the group's last row has nothing to read or store (warp-uniform)
       if (wrows > 0)
-        epilogue_tile<MODE, OutT, I8>(taddr, stage, lane, wrow0, wrows, tc.n_tile, F, N_out, gate_of_row, out,
-                                      token_of_row, n_tokens, err, gs, 0, BN / 32, ws);
+        epilogue_tile<MODE, OutT>(taddr, stage, lane, wrow0, wrows, tc.n_tile, F, N_out, gate_of_row, out,
+                                  token_of_row, n_tokens, err, gs);
       tc_fence_before();
       mbar_arrive(bar_tempty + 8 * acc);
     }
@@ -484,7 +470,9 @@ constexpr int B2_STAGE = BM * BK * 2;                        // 128 B-rows per C
 // output columns, and five stages to make room for their staging.  With K <= 512 a tile
 // has at most 8 k-blocks and its 256-column fp32 epilogue, not the operand stream, sets
 // the pace; at longer K the sixth stage is worth more (measured).
-template <bool WIDE>
+// I8: each epilogue warp keeps the tile's 256 column scales in shared memory, fetched while the
+// tile's MMAs run.
+template <bool WIDE, bool I8 = false>
 struct PairCfg {
   static constexpr int stages = WIDE ? 5 : 6;
   static constexpr int epi_warps = WIDE ? 8 : 4;
@@ -497,19 +485,20 @@ struct PairCfg {
   static constexpr int tiles = misc + 16;
   static constexpr int sh32 = tiles + (kMaxE + 1) * 4;
   static constexpr int stage = (sh32 + 32 * 4 + 15) / 16 * 16;
-  static constexpr int end = stage + epi_warps * kStageWarpBytes;
+  static constexpr int scales = stage + epi_warps * kStageWarpBytes;
+  static constexpr int end = scales + (I8 ? epi_warps * BN * 4 : 0);
   static constexpr size_t smem = end + 1024;
   static_assert(smem <= 232448, "shared memory per CTA");
 };
 
 template <int MODE, typename OutT, bool WIDE, bool I8 = false>
-__global__ void __launch_bounds__(PairCfg<WIDE>::threads, 1)
+__global__ void __launch_bounds__(PairCfg<WIDE, I8>::threads, 1)
 grouped_gemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const int32_t* __restrict__ offsets, int E, int K, int N_out, int F,
                         long long rows_max, const float* __restrict__ gate_of_row,
                         OutT* __restrict__ out, const int32_t* __restrict__ token_of_row, int n_tokens,
                         int* err, const float* __restrict__ row_scale, const float* __restrict__ w_scale) {
-  using C = PairCfg<WIDE>;
+  using C = PairCfg<WIDE, I8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -568,8 +557,9 @@ grouped_gemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
 #pragma unroll
       for (int s = 0; s < C::stages; ++s) last_phase[s] = -1;
       bool ok = true;
+      int e_at = 0;
       for (int tile = cid; ok && tile < total; tile += ncl) {
-        const TileCoord tc = tile_coord(tile_start, offsets, E, PM, tile);
+        const TileCoord tc = tile_coord_next(tile_start, offsets, E, PM, tile, e_at);
         const int a_row = tc.row0 + (int)rank * BM;
         int b_row;
         if (MODE == 0) b_row = tc.e * 2 * F + (rank ? F : 0) + tc.n_tile * 128;   // even: gate, odd: up
@@ -627,9 +617,9 @@ grouped_gemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
     const int c_begin = WIDE ? (ew >> 2) * 4 : 0;            // its column chunks
     const int c_end = WIDE ? c_begin + 4 : BN / 32;
     uint8_t* stage = smem + C::stage + ew * kStageWarpBytes;
-    int it = 0;
+    int it = 0, e_at = 0;
     for (int tile = cid; tile < total; tile += ncl, ++it) {
-      const TileCoord tc = tile_coord(tile_start, offsets, E, PM, tile);
+      const TileCoord tc = tile_coord_next(tile_start, offsets, E, PM, tile, e_at);
       const int acc = it & 1;
       const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
       const int cta_rows = min(BM, max(0, tc.rows - (int)rank * BM));
@@ -638,17 +628,27 @@ grouped_gemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
       // the row's gate, fetched while the tile's MMAs still run
       float gs = ((MODE == 1 || MODE == 3) && lane < wrows && gate_of_row) ? __ldg(gate_of_row + wrow0 + lane) : 1.f;
       if (I8) gs *= lane < wrows ? __ldg(row_scale + wrow0 + lane) : 0.f;
-      const float* ws = I8 ? w_scale + (long long)tc.e * (MODE == 0 ? 2 * F : N_out) : nullptr;
+      float* cs = reinterpret_cast<float*>(smem + C::scales) + ew * BN;
+      if (I8 && wrows > 0) {
+        const float* p = w_scale + (long long)tc.e * (MODE == 0 ? 2 * F : N_out);
+#pragma unroll
+        for (int i = 0; i < BN / 32; ++i) {
+          const int col = i * 32 + lane;                     // of the 256; MODE 0: 128 gate, 128 up
+          const int f = MODE == 0 ? tc.n_tile * 128 + (col & 127) : tc.n_tile * BN + col;
+          const bool in = f < (MODE == 0 ? F : N_out);
+          cs[col] = in ? __ldg(p + (MODE == 0 && col >= 128 ? F + f : f)) : 0.f;
+        }
+      }
       const bool got = mbar_wait(bar_tfull + 8 * acc, acc_phase, abort_flag, err);
       if (!__all_sync(0xffffffffu, got)) break;
-      __syncwarp();
+      __syncwarp();                                          // and the scales are written
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
       // a warp past the group's last row has nothing to read or store (warp-uniform): with
       // many small groups most of a 256-row tile is padding
       if (wrows > 0)
         epilogue_tile<MODE, OutT, I8>(taddr, stage, lane, wrow0, wrows, tc.n_tile, F, N_out, gate_of_row, out,
-                                      token_of_row, n_tokens, err, gs, c_begin, c_end, ws);
+                                      token_of_row, n_tokens, err, gs, c_begin, c_end, cs);
       tc_fence_before();
       mbar_arrive_remote(map_to_rank(bar_tempty + 8 * acc, 0));
     }
@@ -662,23 +662,22 @@ grouped_gemm_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
   }
 }
 
-template <int MODE, typename OutT, bool I8 = false>
+template <int MODE, typename OutT>
 moe_status launch_tc(const CUtensorMap& ma, const CUtensorMap& mb, const int32_t* offsets, int E, int K, int N_out,
                      int F, long long rows_max, const float* gate_of_row, void* out, cudaStream_t s,
                      const int32_t* token_of_row = nullptr, int n_tokens = 0,
-                     const __nv_bfloat16* a_gather = nullptr, const float* row_scale = nullptr,
-                     const float* w_scale = nullptr) {
+                     const __nv_bfloat16* a_gather = nullptr) {
   static std::atomic<int> configured[kMaxDevices];
-  const moe_status st = ensure_smem_limit(configured, grouped_gemm_tc_kernel<MODE, OutT, I8>, kSmemBytes);
+  const moe_status st = ensure_smem_limit(configured, grouped_gemm_tc_kernel<MODE, OutT>, kSmemBytes);
   if (st != MOE_OK) return st;
   const int n_tiles = n_tiles_of<MODE>(F, N_out);
   const long long max_tiles = ((rows_max + BM - 1) / BM + E) * (long long)n_tiles;
   int grid = num_sms();
   if (max_tiles < grid) grid = (int)max_tiles;
   if (grid < 1) grid = 1;
-  grouped_gemm_tc_kernel<MODE, OutT, I8><<<grid, kThreadsTC, kSmemBytes, s>>>(
+  grouped_gemm_tc_kernel<MODE, OutT><<<grid, kThreadsTC, kSmemBytes, s>>>(
       ma, mb, offsets, E, K, N_out, F, rows_max, gate_of_row, static_cast<OutT*>(out), token_of_row, n_tokens,
-      a_gather, err_ptr(), row_scale, w_scale);
+      a_gather, err_ptr());
   return check_launch();
 }
 
@@ -710,7 +709,7 @@ moe_status launch_tc2(const CUtensorMap& ma, const CUtensorMap& mb, const int32_
                       const float* w_scale = nullptr) {
   static std::atomic<int> configured[kMaxDevices];
   const moe_status st =
-      ensure_smem_limit(configured, grouped_gemm_tc2_kernel<MODE, OutT, WIDE, I8>, PairCfg<WIDE>::smem);
+      ensure_smem_limit(configured, grouped_gemm_tc2_kernel<MODE, OutT, WIDE, I8>, PairCfg<WIDE, I8>::smem);
   if (st != MOE_OK) return st;
   const int n_tiles = n_tiles_of<MODE>(F, N_out);
   const long long max_tiles = ((rows_max + 2 * BM - 1) / (2 * BM) + E) * (long long)n_tiles;
@@ -719,8 +718,8 @@ moe_status launch_tc2(const CUtensorMap& ma, const CUtensorMap& mb, const int32_
   if (pairs < 1) pairs = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  cfg.blockDim = dim3(PairCfg<WIDE>::threads, 1, 1);
-  cfg.dynamicSmemBytes = PairCfg<WIDE>::smem;
+  cfg.blockDim = dim3(PairCfg<WIDE, I8>::threads, 1, 1);
+  cfg.dynamicSmemBytes = PairCfg<WIDE, I8>::smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -831,7 +830,9 @@ moe_status launch_gate_up_gather_tc(const void* x, const int32_t* token_of_row, 
 
 // ---- 8-bit operands: x_q or h_q [rows_max, K] and the weights [E][N][K] are signed bytes, read by
 // the same tiles as rows of K / 2 two-byte elements (K a multiple of 16); the accumulators are
-// exact int32 sums and the epilogue multiplies them by the row's and the column's scale. ----
+// exact int32 sums and the epilogue multiplies them by the row's and the column's scale.  A k-block
+// holds twice the products of a bf16 one, so the epilogue has half the time: CTA pairs with eight
+// epilogue warps here, and weight-major tiles below 1024 rows an expert, for the down GEMM too. ----
 moe_status launch_gate_up_i8(const int8_t* x_q, const float* x_scale, const int32_t* offsets, int E, int d, int F,
                              long long rows_max, const int8_t* W, const float* w_scale, void* h, cudaStream_t s) {
   if (prefer_weight_major(rows_max, E, false))
@@ -839,41 +840,25 @@ moe_status launch_gate_up_i8(const int8_t* x_q, const float* x_scale, const int3
   const int K = d / 2;
   CUtensorMap ma, mb;
   if (!make_map(&ma, x_q, (unsigned long long)rows_max, K, BM)) return MOE_ERR_UNSUPPORTED;
-  if (!make_map(&mb, W, (unsigned long long)E * 2 * F, K, 128)) return MOE_ERR_UNSUPPORTED;
-  if (use_pairs(rows_max, E))
-    return launch_tc2<0, __nv_bfloat16, false, true>(ma, mb, offsets, E, K, F, F, rows_max, nullptr, h, s, nullptr, 0,
-                                                     x_scale, w_scale);
-  return launch_tc<0, __nv_bfloat16, true>(ma, mb, offsets, E, K, F, F, rows_max, nullptr, h, s, nullptr, 0, nullptr,
-                                           x_scale, w_scale);
+  if (!make_map(&mb, W, (unsigned long long)E * 2 * F, K, BM)) return MOE_ERR_UNSUPPORTED;
+  return launch_tc2<0, __nv_bfloat16, true, true>(ma, mb, offsets, E, K, F, F, rows_max, nullptr, h, s, nullptr, 0,
+                                                  x_scale, w_scale);
 }
 
 moe_status launch_down_i8(const int8_t* h_q, const float* h_scale, const int32_t* offsets, int E, int d, int F,
                           long long rows_max, const int8_t* W, const float* w_scale, const float* gate_of_row,
                           int y_dtype, void* y_rows, cudaStream_t s) {
-  if (prefer_weight_major(rows_max, E, true))
+  if (prefer_weight_major(rows_max, E, false))
     return launch_down_wm_i8(h_q, h_scale, offsets, E, d, F, rows_max, W, w_scale, gate_of_row, y_dtype, y_rows, s);
   const int K = F / 2;
-  const bool pair = use_pairs(rows_max, E);
   CUtensorMap ma, mb;
   if (!make_map(&ma, h_q, (unsigned long long)rows_max, K, BM)) return MOE_ERR_UNSUPPORTED;
-  if (!make_map(&mb, W, (unsigned long long)E * d, K, pair ? BM : BN)) return MOE_ERR_UNSUPPORTED;
-#define MOE_PAIR(T, WIDE)                                                                                        \
-  return launch_tc2<1, T, WIDE, true>(ma, mb, offsets, E, K, d, F, rows_max, gate_of_row, y_rows, s, nullptr, 0, \
-                                      h_scale, w_scale)
-  if (pair && K <= kWideMaxK) {
-    if (y_dtype == MOE_F32) MOE_PAIR(float, true);
-    MOE_PAIR(__nv_bfloat16, true);
-  }
-  if (pair) {
-    if (y_dtype == MOE_F32) MOE_PAIR(float, false);
-    MOE_PAIR(__nv_bfloat16, false);
-  }
-#undef MOE_PAIR
+  if (!make_map(&mb, W, (unsigned long long)E * d, K, BM)) return MOE_ERR_UNSUPPORTED;
   if (y_dtype == MOE_F32)
-    return launch_tc<1, float, true>(ma, mb, offsets, E, K, d, F, rows_max, gate_of_row, y_rows, s, nullptr, 0,
-                                     nullptr, h_scale, w_scale);
-  return launch_tc<1, __nv_bfloat16, true>(ma, mb, offsets, E, K, d, F, rows_max, gate_of_row, y_rows, s, nullptr, 0,
-                                           nullptr, h_scale, w_scale);
+    return launch_tc2<1, float, true, true>(ma, mb, offsets, E, K, d, F, rows_max, gate_of_row, y_rows, s, nullptr, 0,
+                                            h_scale, w_scale);
+  return launch_tc2<1, __nv_bfloat16, true, true>(ma, mb, offsets, E, K, d, F, rows_max, gate_of_row, y_rows, s,
+                                                  nullptr, 0, h_scale, w_scale);
 }
 
 }  // namespace moe

@@ -28,6 +28,7 @@
 // tile overlap the next tile's mainloop.  Every wait is bounded (MOE_DEVERR_PIPE_TIMEOUT,
 // then an orderly exit).  No load uses cluster multicast.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "tc_prims.cuh"
 #include "tile_sched.cuh"
 
@@ -41,14 +42,16 @@ constexpr int kWBlock = kWRows * BK * 2;       // 16 KB: one 128-row operand blo
 constexpr int kFp4PadRows = 2 * kWRows;        // zero rows after the prepared 4-bit scales
 constexpr int kWXBox = 16;                      // token rows per TMA box: a tile loads only its n / 2 rows
 
-template <int MODE>
+// 8-bit down GEMM: its tiles have half the k-blocks, so eight epilogue warps (two a TMEM lane
+// quarter, every other chunk of 32 tokens each) in place of the sixth stage.
+template <int MODE, bool I8 = false>
 struct WmCfg {
   static constexpr int NT = MODE == 0 ? 128 : 256;            // tokens per tile (MMA N at most)
   static constexpr int a_blocks = MODE == 0 ? 2 : 1;           // gate + up, or down
   static constexpr int b_bytes = (NT / 2) * BK * 2;            // this CTA's token rows per stage
   static constexpr int stage_bytes = a_blocks * kWBlock + b_bytes;
-  static constexpr int stages = MODE == 0 ? 5 : 6;
-  static constexpr int epi_warps = 4;
+  static constexpr int stages = MODE == 0 || I8 ? 5 : 6;
+  static constexpr int epi_warps = MODE == 1 && I8 ? 8 : 4;
   static constexpr int threads = 64 + 32 * epi_warps;
   static constexpr int bars = stages * stage_bytes;
   static constexpr int nbars = 2 * stages + 4 + 1;   // full, empty, tfull[2], tempty[2], fin
@@ -56,7 +59,8 @@ struct WmCfg {
   static constexpr int tiles = misc + 16;
   static constexpr int sh32 = tiles + (kWMaxE + 1) * 4;
   static constexpr int stage = (sh32 + 32 * 4 + 127) / 128 * 128;
-  static constexpr int end = stage + epi_warps * kStageWarpBytes;
+  static constexpr int factors = stage + epi_warps * kStageWarpBytes;   // I8: 32 row factors a warp
+  static constexpr int end = factors + (I8 ? epi_warps * 128 : 0);
   static constexpr size_t smem = end + 1024;
   static_assert(smem <= 232448, "shared memory per CTA");
   static_assert(stage_bytes % 1024 == 0, "stages must keep the 1024-byte swizzle alignment");
@@ -138,16 +142,11 @@ __device__ __forceinline__ float wm_row_scale(const float* __restrict__ row_scal
 //   MODE 1: y[token][n] = gate_of_row[token] * wscale * acc.
 // g0, g1 (MODE 1): this lane's gates of the tile's first two 32-token chunks, fetched by the
 // caller before the accumulator was ready; later gates are fetched one chunk pair ahead.
-// I8 (int32 accumulators): wscale and uscale are this lane's feature's weight scales (MODE 0:
-// gate and up; MODE 1: wscale alone), and the rows' scales come from row_scale.
-template <int MODE, typename OutT, bool I8 = false>
+template <int MODE, typename OutT>
 __device__ __forceinline__ void wm_epilogue_tile(uint32_t taddr, uint8_t* stage, int lane, const TileCoord& tc,
                                                  int rank, int q, int d, int F, float wscale,
                                                  const float* __restrict__ gate_of_row, OutT* __restrict__ out,
-                                                 float g0 = 1.f, float g1 = 1.f, float uscale = 1.f,
-                                                 const float* __restrict__ row_scale = nullptr,
-                                                 const int32_t* __restrict__ token_of_row = nullptr,
-                                                 int n_tokens = 0) {
+                                                 float g0 = 1.f, float g1 = 1.f) {
   const int col0 = tc.n_tile * 256 + rank * kWRows + q * 32;   // this warp's first feature
   const int chunks = (tc.rows + 31) / 32;
   if constexpr (MODE == 0) {
@@ -155,7 +154,6 @@ __device__ __forceinline__ void wm_epilogue_tile(uint32_t taddr, uint8_t* stage,
     for (int c = 0; c < chunks; ++c) {
       const long long r0 = (long long)tc.row0 + c * 32;
       const int rv = min(32, tc.rows - c * 32);
-      const float sr = I8 ? wm_row_scale(row_scale, token_of_row, n_tokens, tc, c, lane) : 1.f;
       float h[32];
       uint32_t g[32], u[32];
       tmem_ld32(taddr + c * 32, g);
@@ -165,34 +163,18 @@ __device__ __forceinline__ void wm_epilogue_tile(uint32_t taddr, uint8_t* stage,
       tmem_regs_ready(u);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        float gi, ui;
-        if constexpr (I8) {
-          const float si = __shfl_sync(0xffffffffu, sr, i);
-          gi = acc_value<true>(g[i]) * (si * wscale);
-          ui = acc_value<true>(u[i]) * (si * uscale);
-        } else {
-          gi = __uint_as_float(g[i]) * wscale;
-          ui = __uint_as_float(u[i]) * wscale;
-        }
+        const float gi = __uint_as_float(g[i]) * wscale;
         // fast exp / divide: H is rounded to bf16 next, far coarser than their error
-        h[i] = __fdividef(gi, 1.f + __expf(-gi)) * ui;
+        h[i] = __fdividef(gi, 1.f + __expf(-gi)) * (__uint_as_float(u[i]) * wscale);
       }
       stage_store32_t<OutT>(stage, h, lane, out, r0, rv, F, col0, F);
     }
   } else {
     // two 32-token chunks per TMEM wait (the tile's mainloop is only K / 64 k-blocks)
     float ga = g0, gb = g1;
-    if (I8) {
-      ga *= wm_row_scale(row_scale, nullptr, 0, tc, 0, lane);
-      gb *= wm_row_scale(row_scale, nullptr, 0, tc, 1, lane);
-    }
 #pragma unroll 1
     for (int c = 0; c < chunks; c += 2) {
-      float na = wm_gate(gate_of_row, tc, c + 2, lane), nb = wm_gate(gate_of_row, tc, c + 3, lane);
-      if (I8) {
-        na *= wm_row_scale(row_scale, nullptr, 0, tc, c + 2, lane);
-        nb *= wm_row_scale(row_scale, nullptr, 0, tc, c + 3, lane);
-      }
+      const float na = wm_gate(gate_of_row, tc, c + 2, lane), nb = wm_gate(gate_of_row, tc, c + 3, lane);
       const bool two = c + 1 < chunks;                     // warp-uniform
       uint32_t v[32], vb[32];
       tmem_ld32(taddr + c * 32, v);
@@ -201,28 +183,153 @@ __device__ __forceinline__ void wm_epilogue_tile(uint32_t taddr, uint8_t* stage,
       tmem_regs_ready(v);
       tmem_regs_ready(vb);
       float h[32];
-      const float gs = I8 ? ga : ga * wscale;              // I8: wscale is this lane's, not the row's
+      const float gs = ga * wscale;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) h[i] = acc_value<I8>(v[i]) * __shfl_sync(0xffffffffu, gs, i);
-      if (I8) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) h[i] *= wscale;
-      }
+      for (int i = 0; i < 32; ++i) h[i] = __uint_as_float(v[i]) * __shfl_sync(0xffffffffu, gs, i);
       stage_store32_t<OutT>(stage, h, lane, out, (long long)tc.row0 + c * 32, min(32, tc.rows - c * 32), d, col0,
                             d);
       if (two) {
-        const float gsb = I8 ? gb : gb * wscale;
+        const float gsb = gb * wscale;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) h[i] = acc_value<I8>(vb[i]) * __shfl_sync(0xffffffffu, gsb, i);
-        if (I8) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) h[i] *= wscale;
-        }
+        for (int i = 0; i < 32; ++i) h[i] = __uint_as_float(vb[i]) * __shfl_sync(0xffffffffu, gsb, i);
         stage_store32_t<OutT>(stage, h, lane, out, (long long)tc.row0 + (c + 1) * 32,
                               min(32, tc.rows - (c + 1) * 32), d, col0, d);
       }
       ga = na;
       gb = nb;
+    }
+  }
+}
+
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+// 32 tokens x 32 features of bf16 from the warp's staging tile to their rows, 16 bytes a lane; rows
+// past rows_valid and columns past ncols skipped.
+__device__ __forceinline__ void stage_rows32(const uint8_t* stage, int lane, __nv_bfloat16* out, long long row0,
+                                             int rows_valid, long long ld, int col, int ncols) {
+  const int rs = lane >> 2, cv = lane & 3;                 // 8 rows per pass, 4 x 16 B per row
+  if (col + cv * 8 + 8 > ncols) return;
+  __nv_bfloat16* to = out + (row0 + rs) * ld + col + cv * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i * 8 + rs < rows_valid)
+      *reinterpret_cast<uint4*>(to + i * 8 * ld) =
+          *reinterpret_cast<const uint4*>(stage + (i * 8 + rs) * kStagePitchB16 + cv * 16);
+}
+
+constexpr int kI8Chunks = 4;                               // chunks of 32 tokens a warp has of a tile, at most
+// As loaded, nothing computed from them before they are used: a tile's are on their way while the
+// tile before is worked on.
+struct I8Scales {
+  float w, u;                                              // this lane's feature's weight scales
+  float f[kI8Chunks], g[kI8Chunks];                        // its token's scale and gate in each chunk
+};
+
+// The epilogue for int32 accumulators of 8-bit products: the rows' factors (scale, times the gate
+// in MODE 1) pass through `factors`, 32 floats of shared memory; the warp does chunks c0, c0 +
+// step, ...
+// bf16 rows: the accumulators are read as matrix fragments (a thread has pairs of neighbouring
+// tokens of one feature), multiplied and rounded in pairs, and stored transposed, eight by eight,
+// by stmatrix: some 160 instructions for 32 x 32 outputs, half of what one value a lane and step
+// takes.
+template <int MODE, typename OutT>
+__device__ __forceinline__ void wm_epilogue_tile_i8(uint32_t taddr, uint8_t* stage, float* factors, int lane,
+                                                    const TileCoord& tc, int rank, int q, int d, int F,
+                                                    const I8Scales& sc, OutT* __restrict__ out, int c0, int step) {
+  constexpr bool FRAG = sizeof(OutT) == 2;
+  const int chunks = (tc.rows + 31) / 32;
+  const int ld = MODE == 0 ? F : d;
+  const int col0 = tc.n_tile * 256 + rank * kWRows + q * 32;   // this warp's first feature
+  f32x2 ws[4], us[4];                                      // fragments: features lane / 4 + 8 m
+  if constexpr (FRAG) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      ws[m] = both(__shfl_sync(0xffffffffu, sc.w, (lane >> 2) + 8 * m));
+      if constexpr (MODE == 0) us[m] = both(__shfl_sync(0xffffffffu, sc.u, (lane >> 2) + 8 * m));
+    }
+  }
+  auto fetch = [&](uint32_t col, uint32_t (&r)[32]) {
+    if constexpr (FRAG) tmem_ld_frag32(taddr + col, r);
+    else tmem_ld32(taddr + col, r);
+  };
+  auto finish = [&](int c, float f, const uint32_t (&g)[32], const uint32_t* u) {
+    factors[lane] = f;
+    __syncwarp();
+    const long long row0 = (long long)tc.row0 + c * 32;
+    if constexpr (FRAG) {
+      f32x2 s[4];                                          // tokens 8 j + 2 (lane % 4), + 1
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = *reinterpret_cast<const float2*>(factors + 8 * j + 2 * (lane & 3));
+        s[j] = pack2(v.x, v.y);
+      }
+      const uint32_t to = smem_u32(stage) + (uint32_t)(lane * kStagePitchB16);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {                        // eight features
+        uint32_t p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {                      // eight tokens
+          const int r = (m >> 1) * 16 + j * 4 + (m & 1) * 2;
+          float2 h = unpack2(mul2(mul2(pack2(acc_value<true>(g[r]), acc_value<true>(g[r + 1])), s[j]), ws[m]));
+          if constexpr (MODE == 0) {
+            const float2 v =
+                unpack2(mul2(mul2(pack2(acc_value<true>(u[r]), acc_value<true>(u[r + 1])), s[j]), us[m]));
+            h.x = __fdividef(h.x, 1.f + __expf(-h.x)) * v.x;
+            h.y = __fdividef(h.y, 1.f + __expf(-h.y)) * v.y;
+          }
+          p[j] = pack_bf16x2(h.x, h.y);
+        }
+        stmatrix_x4_trans(to + 16 * m, p[0], p[1], p[2], p[3]);   // lane: token `lane`, features 8 m ..
+      }
+      __syncwarp();
+      stage_rows32(stage, lane, out, row0, tc.rows - c * 32, ld, col0, ld);
+      __syncwarp();
+    } else {
+      static_assert(FRAG || MODE == 1, "H is bf16");
+      float h[32];
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const float4 s = *reinterpret_cast<const float4*>(factors + i);
+        h[i] = acc_value<true>(g[i]) * s.x * sc.w;
+        h[i + 1] = acc_value<true>(g[i + 1]) * s.y * sc.w;
+        h[i + 2] = acc_value<true>(g[i + 2]) * s.z * sc.w;
+        h[i + 3] = acc_value<true>(g[i + 3]) * s.w * sc.w;
+      }
+      stage_store32_t<OutT>(stage, h, lane, out, row0, min(32, tc.rows - c * 32), ld, col0, ld);
+    }
+  };
+  uint32_t a[32], b[32];                                   // MODE 0: gate and up; MODE 1: this chunk, the next
+  if constexpr (MODE == 0) {
+#pragma unroll
+    for (int i = 0; i < kI8Chunks; ++i) {
+      const int c = c0 + i * step;
+      if (c >= chunks) break;
+      fetch(c * 32, a);
+      fetch(128 + c * 32, b);
+      tmem_wait_ld();
+      tmem_regs_ready(a);
+      tmem_regs_ready(b);
+      finish(c, sc.f[i], a, b);
+    }
+  } else {
+    if (c0 < chunks) fetch(c0 * 32, a);
+#pragma unroll
+    for (int i = 0; i < kI8Chunks; i += 2) {
+      const int c = c0 + i * step;
+      if (c >= chunks) break;
+      tmem_wait_ld();
+      tmem_regs_ready(a);
+      const bool more = c + step < chunks;                 // warp-uniform, like every branch here
+      if (more) fetch((c + step) * 32, b);
+      finish(c, sc.f[i] * sc.g[i], a, nullptr);
+      if (!more) break;
+      tmem_wait_ld();
+      tmem_regs_ready(b);
+      if (c + 2 * step < chunks) fetch((c + 2 * step) * 32, a);
+      finish(c + step, sc.f[i + 1] * sc.g[i + 1], b, nullptr);
     }
   }
 }
@@ -234,14 +341,14 @@ __device__ __forceinline__ void wm_epilogue_tile(uint32_t taddr, uint8_t* stage,
 // I8: 8-bit rows and weights, read as rows of K two-byte elements (K = bytes / 2); row_scale by
 // row (GATHER: by token), w_scale [E][2F] or [E][d].
 template <int MODE, typename OutT, bool GATHER = false, bool I8 = false>
-__global__ void __launch_bounds__(WmCfg<MODE>::threads, 1)
+__global__ void __launch_bounds__(WmCfg<MODE, I8>::threads, 1)
 grouped_gemm_wm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                        const int32_t* __restrict__ offsets, int E, int K, int d, int F, long long rows_max,
                        const float* __restrict__ gate_of_row, OutT* __restrict__ out, int* err,
                        const int32_t* __restrict__ token_of_row = nullptr, int n_tokens = 0,
                        const float* __restrict__ row_scale = nullptr, const float* __restrict__ w_scale = nullptr) {
   static_assert(!GATHER || MODE == 0, "the gathered form is the gate/up GEMM's");
-  using C = WmCfg<MODE>;
+  using C = WmCfg<MODE, I8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -303,8 +410,9 @@ grouped_gemm_wm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_con
 #pragma unroll
     for (int s = 0; s < C::stages; ++s) last_phase[s] = -1;
     bool ok = true;
+    int e_at = 0;
     for (int tile = cid; ok && tile < total; tile += ncl) {
-      const TileCoord tc = tile_coord(tile_start, offsets, E, C::NT, tile);
+      const TileCoord tc = tile_coord_next(tile_start, offsets, E, C::NT, tile, e_at);
       const int half = wm_n<MODE>(tc.rows) / 2;
       const int w_row = tc.e * 2 * F + tc.n_tile * 256 + (int)rank * kWRows;
       const bool mine = 4 * lane < half;
@@ -350,8 +458,9 @@ grouped_gemm_wm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_con
 #pragma unroll
       for (int s = 0; s < C::stages; ++s) last_phase[s] = -1;
       bool ok = true;
+      int e_at = 0;
       for (int tile = cid; ok && tile < total; tile += ncl) {
-        const TileCoord tc = tile_coord(tile_start, offsets, E, C::NT, tile);
+        const TileCoord tc = tile_coord_next(tile_start, offsets, E, C::NT, tile, e_at);
         const int n = wm_n<MODE>(tc.rows);
         // this CTA's weight rows, and its half of the tile's tokens (columns [rank n/2, ...))
         const int w_row = MODE == 0 ? tc.e * 2 * F + tc.n_tile * 256 + (int)rank * kWRows
@@ -382,10 +491,11 @@ grouped_gemm_wm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_con
       uint32_t phase = 0;
       int it = 0;
       bool ok = true;
+      int e_at = 0;
       for (int tile = cid; ok && tile < total; tile += ncl, ++it) {
         const int acc = it & 1;
         const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-        const TileCoord tc = tile_coord(tile_start, offsets, E, C::NT, tile);
+        const TileCoord tc = tile_coord_next(tile_start, offsets, E, C::NT, tile, e_at);
         const uint32_t idesc = make_idesc_of<I8>(2 * kWRows, wm_n<MODE>(tc.rows));
         if (!mbar_wait(bar_tempty + 8 * acc, acc_phase ^ 1u, abort_flag, err)) { ok = false; break; }
         tc_fence_after();
@@ -414,31 +524,77 @@ grouped_gemm_wm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_con
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;                                  // TMEM lane quarter of this warp
-    uint8_t* stage = smem + C::stage + (warp - 2) * kStageWarpBytes;
-    int it = 0;
-    for (int tile = cid; tile < total; tile += ncl, ++it) {
-      const TileCoord tc = tile_coord(tile_start, offsets, E, C::NT, tile);
-      const int acc = it & 1;
-      const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-      // the first gates, fetched while the tile's MMAs still run
-      const float g0 = MODE == 1 ? wm_gate(gate_of_row, tc, 0, lane) : 1.f;
-      const float g1 = MODE == 1 ? wm_gate(gate_of_row, tc, 1, lane) : 1.f;
-      float sw = 1.f, su = 1.f;
-      if (I8) {                                              // this lane's feature's weight scales
-        const int f = tc.n_tile * 256 + (int)rank * kWRows + q * 32 + lane, n = MODE == 0 ? F : d;
-        const float* p = w_scale + (long long)tc.e * (MODE == 0 ? 2 * F : d);
-        sw = f < n ? __ldg(p + f) : 0.f;
-        su = MODE == 0 && f < n ? __ldg(p + F + f) : 0.f;
+    const int ew = warp - 2;
+    uint8_t* stage = smem + C::stage + ew * kStageWarpBytes;
+    int it = 0, e_at = 0;
+    if constexpr (I8) {
+      constexpr int groups = C::epi_warps / 4;
+      const int half = ew >> 2;                              // every groups-th chunk, from this one
+      float* factors = reinterpret_cast<float*>(smem + C::factors) + ew * 32;
+      // two tiles ahead its expert's rows are asked for, one tile ahead its scales (an L2 round trip
+      // each, some 1500 cycles a tile of the 4000 that it took when they were waited for)
+      auto scales = [&](const TileCoord& t) {
+        I8Scales s;
+        const int x = t.n_tile * 256 + (int)rank * kWRows + q * 32 + lane, n = MODE == 0 ? F : d;
+        const float* p = w_scale + (long long)t.e * (MODE == 0 ? 2 * F : d);
+        s.w = x < n ? __ldg(p + x) : 0.f;
+        s.u = MODE == 0 && x < n ? __ldg(p + F + x) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kI8Chunks; ++i) {
+          const int c = half + i * groups;
+          s.f[i] = wm_row_scale(row_scale, GATHER ? token_of_row : nullptr, n_tokens, t, c, lane);
+          s.g[i] = MODE == 1 ? wm_gate(gate_of_row, t, c, lane) : 1.f;
+        }
+        return s;
+      };
+      int e1 = 0, a1 = 0, b1 = 0;                            // the next tile's expert and its rows
+      auto ask = [&](int tile) {
+        e_at = tile_expert_next(tile_start, E, tile, e_at);
+        e1 = e_at;
+        a1 = __ldg(offsets + e1);
+        b1 = __ldg(offsets + e1 + 1);
+      };
+      TileCoord tc = tile_coord_next(tile_start, offsets, E, C::NT, cid, e_at);
+      I8Scales sc = scales(tc);
+      if (cid + ncl < total) ask(cid + ncl);
+      for (int tile = cid; tile < total; tile += ncl, ++it) {
+        const int acc = it & 1;
+        const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+        TileCoord nx = tc;
+        I8Scales ns = sc;
+        if (tile + ncl < total) {
+          nx = tile_coord_in(tile_start, a1, b1, C::NT, tile + ncl, e1);
+          ns = scales(nx);
+          if (tile + 2 * ncl < total) ask(tile + 2 * ncl);
+        }
+        const bool got = mbar_wait(bar_tfull + 8 * acc, acc_phase, abort_flag, err);
+        if (!__all_sync(0xffffffffu, got)) break;
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
+        wm_epilogue_tile_i8<MODE, OutT>(taddr, stage, factors, lane, tc, (int)rank, q, d, F, sc, out, half, groups);
+        tc_fence_before();
+        mbar_arrive_remote(map_to_rank(bar_tempty + 8 * acc, 0));
+        tc = nx;
+        sc = ns;
       }
-      const bool got = mbar_wait(bar_tfull + 8 * acc, acc_phase, abort_flag, err);
-      if (!__all_sync(0xffffffffu, got)) break;
-      __syncwarp();
-      tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
-      wm_epilogue_tile<MODE, OutT, I8>(taddr, stage, lane, tc, (int)rank, q, d, F, sw, gate_of_row, out, g0, g1, su,
-                                       row_scale, GATHER ? token_of_row : nullptr, n_tokens);
-      tc_fence_before();
-      mbar_arrive_remote(map_to_rank(bar_tempty + 8 * acc, 0));
+    } else {
+      for (int tile = cid; tile < total; tile += ncl, ++it) {
+        const TileCoord tc = tile_coord_next(tile_start, offsets, E, C::NT, tile, e_at);
+        const int acc = it & 1;
+        const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+        // the first gates, fetched while the tile's MMAs still run
+        const float g0 = MODE == 1 ? wm_gate(gate_of_row, tc, 0, lane) : 1.f;
+        const float g1 = MODE == 1 ? wm_gate(gate_of_row, tc, 1, lane) : 1.f;
+        const bool got = mbar_wait(bar_tfull + 8 * acc, acc_phase, abort_flag, err);
+        if (!__all_sync(0xffffffffu, got)) break;
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 256);
+        wm_epilogue_tile<MODE, OutT>(taddr, stage, lane, tc, (int)rank, q, d, F, 1.f, gate_of_row, out, g0, g1);
+        tc_fence_before();
+        mbar_arrive_remote(map_to_rank(bar_tempty + 8 * acc, 0));
+      }
     }
   }
 
@@ -834,7 +990,7 @@ moe_status launch_wm(const CUtensorMap& mw, const CUtensorMap& mx, const int32_t
                      int F, long long rows_max, const float* gate_of_row, void* out, cudaStream_t s,
                      const int32_t* token_of_row = nullptr, int n_tokens = 0, const float* row_scale = nullptr,
                      const float* w_scale = nullptr) {
-  using C = WmCfg<MODE>;
+  using C = WmCfg<MODE, I8>;
   static std::atomic<int> configured[kMaxDevices];
   const moe_status st = ensure_smem_limit(configured, grouped_gemm_wm_kernel<MODE, OutT, GATHER, I8>, C::smem);
   if (st != MOE_OK) return st;

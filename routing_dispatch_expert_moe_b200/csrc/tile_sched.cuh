@@ -77,26 +77,56 @@ __device__ __forceinline__ void build_tile_starts(const int32_t* __restrict__ of
   __syncthreads();
 }
 
-// Tile index -> coordinates: m fastest inside an expert, then n, so that the CTAs working
-// at one time share each weight tile (the large operand of the expert GEMMs).
-__device__ __forceinline__ TileCoord tile_coord(const int* tile_start, const int32_t* __restrict__ offsets,
-                                                int E, int BM, int tile) {
-  int lo = 0, hi = E;  // find last e with tile_start[e] <= tile
+// The last expert in [lo, E) whose first tile is at or before `tile` (tile_start[lo] <= tile).
+__device__ __forceinline__ int tile_expert(const int* tile_start, int E, int tile, int lo) {
+  int hi = E;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (tile_start[mid] <= tile) lo = mid; else hi = mid;
   }
+  return lo;
+}
+// The same for a role that walks its tiles upwards: from the last tile's expert a few steps, and
+// only past those a search (a search of 10 dependent reads for every tile shows where a tile has
+// few k-blocks).
+__device__ __forceinline__ int tile_expert_next(const int* tile_start, int E, int tile, int lo) {
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    if (lo + 1 >= E || tile_start[lo + 1] > tile) return lo;
+    ++lo;
+  }
+  return tile_expert(tile_start, E, tile, lo);
+}
+
+// Tile index -> coordinates: m fastest inside an expert, then n, so that the CTAs working
+// at one time share each weight tile (the large operand of the expert GEMMs).  a, b: the
+// expert's first row and the one past its last.
+__device__ __forceinline__ TileCoord tile_coord_in(const int* tile_start, int a, int b, int BM, int tile, int lo) {
   // skip experts that own no tile (equal starts): the last e with start <= tile owns it
   TileCoord c;
   c.e = lo;
-  const int a = __ldg(offsets + lo), b = __ldg(offsets + lo + 1);
-  const int mt = (b - a + BM - 1) / BM;
   const int local = tile - tile_start[lo];
-  c.n_tile = local / mt;
-  const int m = local - c.n_tile * mt;
+  int m = 0;
+  c.n_tile = local;
+  if (b - a > BM) {                                        // more than one row tile (else no division)
+    const int mt = (b - a + BM - 1) / BM;
+    c.n_tile = local / mt;
+    m = local - c.n_tile * mt;
+  }
   c.row0 = a + m * BM;
   c.rows = min(BM, b - c.row0);
   return c;
+}
+__device__ __forceinline__ TileCoord tile_coord(const int* tile_start, const int32_t* __restrict__ offsets,
+                                                int E, int BM, int tile) {
+  const int e = tile_expert(tile_start, E, tile, 0);
+  return tile_coord_in(tile_start, __ldg(offsets + e), __ldg(offsets + e + 1), BM, tile, e);
+}
+// As tile_coord, for tiles walked upwards: e holds the last tile's expert (0 at first).
+__device__ __forceinline__ TileCoord tile_coord_next(const int* tile_start, const int32_t* __restrict__ offsets,
+                                                     int E, int BM, int tile, int& e) {
+  e = tile_expert_next(tile_start, E, tile, e);
+  return tile_coord_in(tile_start, __ldg(offsets + e), __ldg(offsets + e + 1), BM, tile, e);
 }
 
 }  // namespace moe

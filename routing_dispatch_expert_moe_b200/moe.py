@@ -707,6 +707,18 @@ class _on:
         return torch._C._cuda_getCurrentRawStream(self.index) if given is None else given.cuda_stream
 
 
+def _want(t: torch.Tensor, name: str, dtype, shape):
+    """_need with both given, checked in one go (the small calls are as long as their checks)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+    return t
+
+
+def _new(shape, dtype, device) -> torch.Tensor:
+    """A dense tensor of one or two dimensions; empty_strided is the quickest way to one."""
+    return torch.empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype=dtype, device=device)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -734,12 +746,12 @@ def moe_route_grouped(logits, k: int, n_groups: int, groups_kept: int, group_sco
     _need(logits, "logits", torch.float32)
     T, E = logits.shape
     if select_bias is not None:
-        _need(select_bias, "select_bias", torch.float32, (E,))
+        _want(select_bias, "select_bias", torch.float32, (E,))
     dev = logits.device
-    topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_idx is None else \
-        _need(topk_idx, "topk_idx", torch.int32, (T, k))
-    topk_gate = torch.empty((T, k), dtype=torch.float32, device=dev) if topk_gate is None else \
-        _need(topk_gate, "topk_gate", torch.float32, (T, k))
+    topk_idx = _new((T, k), torch.int32, dev) if topk_idx is None else \
+        _want(topk_idx, "topk_idx", torch.int32, (T, k))
+    topk_gate = _new((T, k), torch.float32, dev) if topk_gate is None else \
+        _want(topk_gate, "topk_gate", torch.float32, (T, k))
     with _on(logits, select_bias, topk_idx, topk_gate) as on:
         _check("moe_route_grouped", lib().moe_route_grouped(
             _ptr(logits), _ptr(select_bias), T, E, k, n_groups, groups_kept,
@@ -762,10 +774,10 @@ def moe_route_backward(logits, topk_idx=None, d_gate=None, score: str = "softmax
         k = topk_idx.shape[1] if topk_idx.dim() == 2 else 0
         _need(topk_idx, "topk_idx", None, (T, k))
     if d_gate is not None:
-        _need(d_gate, "d_gate", torch.float32, (T, k))
+        _want(d_gate, "d_gate", torch.float32, (T, k))
     if load is not None:
-        _need(load, "load", torch.float32, (E,))
-    d_logits = torch.empty_like(logits) if d_logits is None else _need(d_logits, "d_logits", torch.float32, (T, E))
+        _want(load, "load", torch.float32, (E,))
+    d_logits = torch.empty_like(logits) if d_logits is None else _want(d_logits, "d_logits", torch.float32, (T, E))
     with _on(logits, topk_idx, d_gate, load, d_logits) as on:
         _check("moe_route_backward", lib().moe_route_backward(
             _ptr(logits), _ptr(topk_idx), _ptr(d_gate), T, E, k, _choice(SCORE, score, "score"),
@@ -784,9 +796,9 @@ def moe_quantize_rows_i8(x, row_of=None, rows_max: int = 0, q=None, scale=None, 
         _need(row_of, "row_of", torch.int32)
         k, out = row_of.shape[1], rows_max
         _need(row_of, "row_of", None, (rows, k))
-    q = torch.empty((out, cols), dtype=torch.int8, device=x.device) if q is None else \
+    q = _new((out, cols), torch.int8, x.device) if q is None else \
         _rows_of(q, "q", out, cols, torch.int8)
-    scale = torch.empty((out,), dtype=torch.float32, device=x.device) if scale is None else \
+    scale = _new((out,), torch.float32, x.device) if scale is None else \
         _rows_of(scale, "scale", out, None, torch.float32)
     with _on(x, row_of, q, scale) as on:
         _check("moe_quantize_rows_i8", lib().moe_quantize_rows_i8(
@@ -810,13 +822,13 @@ def moe_expert_gate_up_i8(x_q, x_scale, offsets, W_gu, w_scale, rows_max: int, h
     _need(W_gu, "W_gu", torch.int8)
     E, F2, d = W_gu.shape
     F = F2 // 2
-    _need(w_scale, "w_scale", torch.float32, (E, F2))
-    _need(offsets, "offsets", torch.int32, (E + 1,))
+    _want(w_scale, "w_scale", torch.float32, (E, F2))
+    _want(offsets, "offsets", torch.int32, (E + 1,))
     T = x_q.shape[0]
     rows = rows_max if token_of_row is None else T
     _rows_of(x_q, "x_q", rows, d, torch.int8)
     _rows_of(x_scale, "x_scale", rows, None, torch.float32)
-    h = torch.empty((rows_max, F), dtype=torch.bfloat16, device=x_q.device) if h is None else \
+    h = _new((rows_max, F), torch.bfloat16, x_q.device) if h is None else \
         _rows_of(h, "h", rows_max, F, torch.bfloat16)
     with _on(x_q, x_scale, offsets, W_gu, w_scale, h, token_of_row) as on:
         if token_of_row is None:
@@ -837,13 +849,13 @@ def moe_expert_down_i8(h_q, h_scale, offsets, W_dn, w_scale, rows_max: int, gate
     weights W_dn [E, d, F] int8 with w_scale [E, d], in y_dtype (default: y_rows' dtype, else fp32)."""
     _need(W_dn, "W_dn", torch.int8)
     E, d, F = W_dn.shape
-    _need(w_scale, "w_scale", torch.float32, (E, d))
-    _need(offsets, "offsets", torch.int32, (E + 1,))
+    _want(w_scale, "w_scale", torch.float32, (E, d))
+    _want(offsets, "offsets", torch.int32, (E + 1,))
     _rows_of(h_q, "h_q", rows_max, F, torch.int8)
     _rows_of(h_scale, "h_scale", rows_max, None, torch.float32)
     if gate_of_row is not None:
         _rows_of(gate_of_row, "gate_of_row", rows_max, None, torch.float32)
-    y_rows = torch.empty((rows_max, d), dtype=y_dtype or torch.float32, device=h_q.device) if y_rows is None else \
+    y_rows = _new((rows_max, d), y_dtype or torch.float32, h_q.device) if y_rows is None else \
         _rows_of(y_rows, "y_rows", rows_max, d, y_dtype)
     with _on(h_q, h_scale, offsets, W_dn, w_scale, gate_of_row, y_rows) as on:
         _check("moe_expert_down_i8", lib().moe_expert_down_i8(
@@ -855,7 +867,7 @@ def moe_expert_down_i8(h_q, h_scale, offsets, W_dn, w_scale, rows_max: int, gate
 def _norm_params(d, post_weight, gate, pre_weight):
     for t, n in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
         if t is not None:
-            _need(t, n, torch.float32, (d,))
+            _want(t, n, torch.float32, (d,))
     if gate is None:
         return 1
     _need(gate, "gate", torch.float32)
@@ -867,13 +879,13 @@ def _norm_params(d, post_weight, gate, pre_weight):
 def _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, want_x):
     shape = residual.shape
     if x_out is not None:
-        _need(x_out, "x_out", residual.dtype, shape)
+        _want(x_out, "x_out", residual.dtype, shape)
     elif want_x:
         x_out = torch.empty_like(residual)
     if n_out is not None:
         _need(n_out, "n_out", n_dtype, shape)
     elif pre_weight is not None:
-        n_out = torch.empty(shape, dtype=n_dtype or torch.bfloat16, device=residual.device)
+        n_out = torch.empty_like(residual, dtype=n_dtype or torch.bfloat16)
     return x_out, n_out
 
 
@@ -909,10 +921,10 @@ def moe_combine_norm(residual, y_rows, row_of, rows_max: int, topk_gate=None, sh
     k = row_of.shape[1] if row_of.dim() == 2 else 0
     _need(row_of, "row_of", None, (T, k))
     if topk_gate is not None:
-        _need(topk_gate, "topk_gate", torch.float32, (T, k))
+        _want(topk_gate, "topk_gate", torch.float32, (T, k))
     for t, n in ((shared_y, "shared_y"), (y_out, "y_out")):
         if t is not None:
-            _need(t, n, y_rows.dtype, (T, d))
+            _want(t, n, y_rows.dtype, (T, d))
     G = _norm_params(d, post_weight, gate, pre_weight)
     x_out, n_out = _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, True)
     rt = _dt(residual)
@@ -934,7 +946,7 @@ def moe_block_norm_backward(d_x, d_n, x_out, y=None, post_weight=None, gate=None
     T, d = x_out.shape
     dev = x_out.device
     if d_x is not None:
-        _need(d_x, "d_x", x_out.dtype, (T, d))
+        _want(d_x, "d_x", x_out.dtype, (T, d))
     for t, n in ((d_n, "d_n"), (y, "y")):
         if t is not None:
             _need(t, n, None, (T, d))
@@ -943,7 +955,7 @@ def moe_block_norm_backward(d_x, d_n, x_out, y=None, post_weight=None, gate=None
     def out(t, name, like, dtype):
         if t is not None:
             return _need(t, name, dtype, None if like is None else like.shape)
-        return None if like is None else torch.empty(like.shape, dtype=dtype, device=dev)
+        return None if like is None else torch.empty_like(like, dtype=dtype)
 
     f32 = torch.float32
     d_residual = out(d_residual, "d_residual", x_out, x_out.dtype)
