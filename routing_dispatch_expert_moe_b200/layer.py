@@ -4,7 +4,8 @@ MoELayer owns preallocated device buffers for a maximum token count and runs, on
 stream with no host synchronisation:
 
     moe_route -> moe_histogram_scan
-      (routing="uniform" / "hash": moe_router_logits -> moe_route_fixed;
+      (n_groups > 1: moe_router_logits -> moe_route_grouped;
+       routing="uniform" / "hash": moe_router_logits -> moe_route_fixed;
        routing="noisy": moe_router_logits for W_g and W_noise -> moe_route_noisy)
       dispatch="permute": -> moe_permute -> moe_expert_gate_up
       dispatch="gather":  -> moe_expert_gate_up_gather (reads x through the row map)
@@ -12,6 +13,11 @@ stream with no host synchronisation:
                        with E = 1] -> moe_combine
       combine="fused": [-> shared expert, written into y] -> moe_expert_down_combine
     [-> moe_router_stats]
+      8-bit experts: moe_quantize_rows_i8 (with the permute in it, or of x for the gathered
+                     GEMM) -> moe_expert_gate_up_i8 -> moe_quantize_rows_i8 -> moe_expert_down_i8
+
+MoEBlock stands around a layer: the norm in front of it, and its combine with the post-norm, the
+gate, the scaled residual and the next norm behind it (moe_block_norm, moe_combine_norm).
 
 "rows" sums each token's terms in slot order and is bitwise reproducible; "fused" adds
 them into y with fp32 atomics inside the down GEMM (no gated-row buffer, no combine
@@ -22,7 +28,7 @@ Orchestration only: every step runs in the library's CUDA kernels.
 from __future__ import annotations
 
 from dataclasses import dataclass
-from typing import Optional
+from typing import Optional, Tuple
 
 import torch
 
@@ -32,8 +38,8 @@ from . import moe as M
 @dataclass
 class MoEWeights:
     Wg: torch.Tensor                          # [d, E] f32
-    W_gu: torch.Tensor                        # [E, 2F, d] act dtype (gate rows, then up rows)
-    W_dn: torch.Tensor                        # [E, d, F] act dtype
+    W_gu: Optional[torch.Tensor]              # [E, 2F, d] act dtype (gate rows, then up rows)
+    W_dn: Optional[torch.Tensor]              # [E, d, F] act dtype (both None: 8-bit experts alone)
     logit_offset: Optional[torch.Tensor] = None   # [E] f32
     select_bias: Optional[torch.Tensor] = None    # [E] f32
     W_gu_s: Optional[torch.Tensor] = None     # [1, 2F_s, d] shared expert
@@ -43,6 +49,10 @@ class MoEWeights:
     # used in place of W_gu / W_dn by the expert GEMMs (the shared expert stays bf16)
     W_gu_fp4: Optional[object] = None
     W_dn_fp4: Optional[object] = None
+    # 8-bit routed experts: (int8 [E, 2F, d], f32 [E, 2F]) and (int8 [E, d, F], f32 [E, d]), e.g. from
+    # moe.quantize_experts_i8; used in place of W_gu / W_dn, which may be None
+    W_gu_i8: Optional[Tuple[torch.Tensor, torch.Tensor]] = None
+    W_dn_i8: Optional[Tuple[torch.Tensor, torch.Tensor]] = None
 
 
 class MoELayer:
@@ -50,7 +60,8 @@ class MoELayer:
                  renormalize: bool = True, scale: float = 1.0, capacity: int = -1,
                  rows_dtype: torch.dtype = torch.float32, out_dtype: torch.dtype = torch.float32,
                  combine: str = "rows", dispatch: str = "permute", overlap: bool = True,
-                 routing: str = "learned", hash_seed: int = 0):
+                 routing: str = "learned", hash_seed: int = 0, n_groups: int = 1, groups_kept: int = 1,
+                 group_score: str = "top2"):
         """rows_dtype: gated expert rows (and the shared expert's output); out_dtype: y.
         fp32 (the default) leaves H as the only bf16 rounding inside the layer.
         combine: "rows" (gated rows + ordered combine) or "fused" (down GEMM adds into an
@@ -65,7 +76,19 @@ class MoELayer:
         "hash" (experts from a hash of the token ids given to forward, seeded by
         hash_seed) or "noisy" (noisy top-k with weights.W_noise and the standard normal
         draws given to forward; softmax gating).  The fixed rules keep the learned gates
-        over the chosen experts; the router statistics always use the router logits."""
+        over the chosen experts; the router statistics always use the router logits.
+        n_groups, groups_kept, group_score: the learned top-k within the groups_kept best of
+        n_groups groups of experts (moe_route_grouped); one group is the plain top-k."""
+        self.i8 = weights.W_gu_i8 is not None
+        if self.i8 and (weights.W_dn_i8 is None or weights.W_gu_fp4 is not None or combine != "rows"
+                        or (weights.W_gu is not None and weights.W_gu.dtype != torch.bfloat16)):
+            raise ValueError("8-bit experts need both W_gu_i8 and W_dn_i8, bf16 activations, no 4-bit experts "
+                             "and combine='rows'")
+        if not self.i8 and (weights.W_gu is None or weights.W_dn is None):
+            raise ValueError("W_gu and W_dn are needed without 8-bit experts")
+        if n_groups > 1 and routing != "learned":
+            raise ValueError("groups of experts only apply to the learned top-k")
+        self.n_groups, self.groups_kept, self.group_score = n_groups, groups_kept, group_score
         self.fp4 = weights.W_gu_fp4 is not None
         if self.fp4 and (weights.W_dn_fp4 is None or combine != "rows" or dispatch == "gather"
                          or weights.W_gu.dtype != torch.bfloat16):
@@ -88,15 +111,15 @@ class MoELayer:
         w = weights
         self.w = w
         self.d, self.E = w.Wg.shape
-        self.F = w.W_dn.shape[2]
+        self.F = (w.W_dn_i8[0] if self.i8 else w.W_dn).shape[2]
         self.k, self.T_max = k, T_max
         self.score, self.renormalize, self.scale, self.capacity = score, renormalize, scale, capacity
-        self.dtype = w.W_gu.dtype
+        self.dtype = torch.bfloat16 if self.i8 else w.W_gu.dtype
         self.rows_dtype, self.out_dtype = rows_dtype, out_dtype
         dev = w.Wg.device
         self.device = dev
         E, d, F = self.E, self.d, self.F
-        self.rows_max = M.moe_rows_max(T_max, E, k, capacity)
+        self.rows_max = self.rows_bound = M.moe_rows_max(T_max, E, k, capacity)
         if dispatch == "auto":
             # gathered where the gate/up GEMM takes weight-major tiles (the token rows are its
             # small operand, read once either way); the permute copy otherwise
@@ -114,7 +137,13 @@ class MoELayer:
         self.row_of = torch.empty((T_max, k), dtype=i32, device=dev)
         self.token_of_row = torch.empty(R, dtype=i32, device=dev)
         self.gate_of_row = torch.empty(R, dtype=f32, device=dev)
-        self.x_perm = torch.empty((R, d), dtype=self.dtype, device=dev) if dispatch == "permute" else None
+        self.x_perm = torch.empty((R, d), dtype=self.dtype, device=dev) if dispatch == "permute" and not self.i8 else None
+        if self.i8:
+            n = R if dispatch == "permute" else T_max             # rows per expert row, or per token
+            self.x_q = torch.empty((n, d), dtype=torch.int8, device=dev)
+            self.x_scale = torch.empty(n, dtype=f32, device=dev)
+            self.h_q = torch.empty((R, F), dtype=torch.int8, device=dev)
+            self.h_scale = torch.empty(R, dtype=f32, device=dev)
         self.h = torch.empty((R, F), dtype=self.dtype, device=dev)
         self.y_perm = torch.empty((R, d), dtype=rows_dtype, device=dev) if combine == "rows" else None
         self.y = torch.empty((T_max, d), dtype=out_dtype, device=dev)
@@ -147,13 +176,18 @@ class MoELayer:
     # individual steps (so that a caller can time them one by one)
     def route(self, x, stream=None, token_id=None, noise=None):
         T = x.shape[0]
-        if self.routing == "learned":
+        if self.routing == "learned" and self.n_groups == 1:
             M.moe_route(x, self.w.Wg, self.k, self.score, self.renormalize, self.scale, self.w.logit_offset,
                         self.w.select_bias, self.logits[:T], self.topk_idx[:T], self.topk_gate[:T], self.ws, stream,
                         Wg_split=self.Wg_split)
             return
         M.moe_router_logits(x, self.w.Wg, self.w.logit_offset, self.logits[:T], self.ws, stream,
                             Wg_split=self.Wg_split)
+        if self.routing == "learned":
+            M.moe_route_grouped(self.logits[:T], self.k, self.n_groups, self.groups_kept, self.group_score, self.score,
+                                self.renormalize, self.scale, self.w.select_bias, self.topk_idx[:T],
+                                self.topk_gate[:T], stream)
+            return
         if self.routing == "noisy":
             if noise is None:
                 raise ValueError("noisy routing needs the standard normal draws (noise=[T, E] f32)")
@@ -169,13 +203,21 @@ class MoELayer:
                           self.topk_gate[:T], stream)
 
     def histogram_scan(self, T, stream=None):
+        self.rows_bound = M.moe_rows_max(T, self.E, self.k, self.capacity)   # rows this batch can have
         M.moe_histogram_scan(self.topk_idx[:T], self.topk_gate[:T], self.E, self.capacity, self.counts, self.kept,
                              self.offsets, self.row_of[:T], self.token_of_row, self.gate_of_row, self.ws, stream)
 
     def permute(self, x, stream=None):
+        if self.i8:                                               # to 8 bits on the way
+            M.moe_quantize_rows_i8(x, self.row_of[:x.shape[0]], self.rows_bound, self.x_q, self.x_scale, stream)
+            return
         M.moe_permute(x, self.row_of[:x.shape[0]], self.rows_max, self.x_perm, stream)
 
     def gate_up(self, stream=None):
+        if self.i8:
+            M.moe_expert_gate_up_i8(self.x_q, self.x_scale, self.offsets, *self.w.W_gu_i8, self.rows_bound, self.h,
+                                    stream=stream)
+            return
         if self.fp4:
             M.moe_expert_gate_up_fp4(self.x_perm, self.offsets, self.w.W_gu_fp4, self.E, self.F, self.rows_max,
                                      self.h, stream)
@@ -183,9 +225,21 @@ class MoELayer:
         M.moe_expert_gate_up(self.x_perm, self.offsets, self.w.W_gu, self.rows_max, self.h, stream)
 
     def gate_up_gather(self, x, stream=None):
+        if self.i8:
+            T = x.shape[0]
+            M.moe_quantize_rows_i8(x, q=self.x_q[:T], scale=self.x_scale[:T], stream=stream)
+            M.moe_expert_gate_up_i8(self.x_q[:T], self.x_scale[:T], self.offsets, *self.w.W_gu_i8, self.rows_bound,
+                                    self.h, self.token_of_row, stream)
+            return
         M.moe_expert_gate_up_gather(x, self.token_of_row, self.offsets, self.w.W_gu, self.rows_max, self.h, stream)
 
     def down(self, stream=None):
+        if self.i8:
+            n = self.rows_bound
+            M.moe_quantize_rows_i8(self.h[:n], q=self.h_q, scale=self.h_scale, stream=stream)
+            M.moe_expert_down_i8(self.h_q, self.h_scale, self.offsets, *self.w.W_dn_i8, n, self.gate_of_row,
+                                 self.y_perm, stream=stream)
+            return
         if self.fp4:
             M.moe_expert_down_fp4(self.h, self.offsets, self.w.W_dn_fp4, self.E, self.d, self.rows_max,
                                   self.gate_of_row, self.y_perm, stream=stream)
@@ -246,8 +300,9 @@ class MoELayer:
         return st
 
     def forward(self, x: torch.Tensor, stream=None, with_stats: bool = True, marks=None, token_id=None,
-                noise=None) -> torch.Tensor:
-        """marks: optional {stage name: (event, event)} recorded on the main stream right
+                noise=None, combine=None) -> torch.Tensor:
+        """combine: a function (T, stream) run in place of the ordered combine (combine="rows"), whose
+        output then is the caller's own; y is not written.  marks: optional {stage name: (event, event)} recorded on the main stream right
         before and after that stage (for timing one kernel inside the real schedule).
         token_id ([T] int32, routing="hash") and noise ([T, E] f32, routing="noisy") are
         that batch's inputs of the routing rule."""
@@ -256,6 +311,8 @@ class MoELayer:
             raise ValueError(f"T={T} exceeds T_max={self.T_max}")
         if x.dtype != self.dtype:
             raise ValueError(f"x must be {self.dtype}")
+        if combine is not None and self.combine_mode != "rows":
+            raise ValueError("another combine needs combine='rows'")
         s = torch.cuda.current_stream() if stream is None else stream
 
         def run(name, fn):
@@ -268,6 +325,8 @@ class MoELayer:
 
         if not self.overlap:
             for name, fn in self.stages(x, with_stats, token_id, noise):
+                if name == "combine" and combine is not None:
+                    fn = lambda s_: combine(T, s_)
                 run(name, fn)
             return self.y[:T]
         side = self._side
@@ -299,7 +358,7 @@ class MoELayer:
             run("down", lambda s_: self.down(s_))
             if self.has_shared:
                 run("shared", lambda s_: self.shared(x, s_))
-            run("combine", lambda s_: self.combine(T, s_))
+            run("combine", lambda s_: (combine or self.combine)(T, s_))
             self._ev_join.record(side)
             s.wait_event(self._ev_join)
         return self.y[:T]
@@ -334,14 +393,14 @@ class MoELayer:
         """Router kernels: one tensor-core kernel (top-k and gates in its epilogue, plus a
         top-k pass for softmax scores with a selection bias), or the SIMT GEMM and top-k."""
         tc = self.dtype == torch.bfloat16 and T >= 256 and self.d >= 64 and self.E % 4 == 0
-        if self.routing == "learned":
+        if self.routing == "learned" and getattr(self, "n_groups", 1) == 1:
             if tc:
                 return 2 if (self.score == "softmax" and self.w.select_bias is not None) else 1
             return 2
         gemm = 1                              # the tensor-core or the SIMT logits kernel
         if self.routing == "noisy":
             return 2 * gemm + 2               # two router GEMMs, the noise pass, the top-k
-        return gemm + 1                       # the GEMM and the fixed selection
+        return gemm + 1                       # the GEMM and the selection by groups or by a fixed rule
 
     def launches_per_forward(self, with_stats: bool = True, T: int = None) -> int:
         T = self.T_max if T is None else T
@@ -350,10 +409,61 @@ class MoELayer:
             n -= 1                         # down_combine (its zero fill is a memset, not a kernel)
             if self.y32 is not self.y:
                 n += 1                     # round_output
-        if self.dispatch_mode == "gather":
+        if getattr(self, "i8", False):
+            n += 1                         # h to 8 bits (x: in the permute's place)
+        elif self.dispatch_mode == "gather":
             n -= 1                         # no permute
         if self.has_shared:
             n += 2
         if with_stats:
             n += 3                         # per-CTA partials, per-expert sums, scalars
         return n
+
+
+class MoEBlock:
+    """An MoE layer with the norms, gate and residual of its transformer block:
+
+        n  = pre_weight * rms_norm(residual)                      (moe_block_norm)
+        y  = the layer's sum over experts of n                    (its stages, without the combine)
+        x' = alpha * residual + gate * post_weight * rms_norm(y)
+        n' = next_weight * rms_norm(x')                           (both with the combine: moe_combine_norm)
+
+    layer: a MoELayer with combine="rows".  pre_weight, post_weight, next_weight: [d] f32 or None;
+    gate: [G, d] f32 or None, G dividing the tokens of every call.  residual_dtype: that of the
+    stream (the normed rows are bf16 or fp32 as the layer takes them).  Buffers for T_max tokens
+    are allocated here; what forward returns are views of them, valid until the next call."""
+
+    def __init__(self, layer: MoELayer, pre_weight, post_weight=None, gate=None, alpha: float = 1.0,
+                 next_weight=None, eps: float = 1e-6, residual_dtype: torch.dtype = torch.bfloat16):
+        if layer.combine_mode != "rows":
+            raise ValueError("a block needs a layer with combine='rows'")
+        if pre_weight is None:
+            raise ValueError("a block needs pre_weight (pass n to forward to skip the norm)")
+        self.layer, self.pre_weight, self.post_weight, self.next_weight = layer, pre_weight, post_weight, next_weight
+        self.gate, self.alpha, self.eps = gate, alpha, eps
+        T, d, dev = layer.T_max, layer.d, layer.device
+        self.n = torch.empty((T, d), dtype=layer.dtype, device=dev)
+        self.x_out = torch.empty((T, d), dtype=residual_dtype, device=dev)
+        self.n_out = torch.empty((T, d), dtype=layer.dtype, device=dev) if next_weight is not None else None
+
+    def forward(self, residual: torch.Tensor, n: Optional[torch.Tensor] = None, stream=None, with_stats: bool = True):
+        """residual [T, d]; n: its pre-norm, where the block before gave it (its n').  Returns
+        (x', n' or None)."""
+        lay, T = self.layer, residual.shape[0]
+        if T > lay.T_max:
+            raise ValueError(f"T={T} exceeds T_max={lay.T_max}")
+        s = torch.cuda.current_stream() if stream is None else stream
+        if n is None:
+            n = self.n[:T]
+            M.moe_block_norm(residual, pre_weight=self.pre_weight, eps=self.eps, n_out=n, stream=s)
+        x_out = self.x_out[:T]
+        n_out = None if self.n_out is None else self.n_out[:T]
+
+        def combine(T_, s_):
+            M.moe_combine_norm(residual, lay.y_perm, lay.row_of[:T_], lay.rows_max,
+                               shared_y=lay.y_s[:T_] if lay.has_shared else None, post_weight=self.post_weight,
+                               gate=self.gate, alpha=self.alpha, pre_weight=self.next_weight, eps=self.eps,
+                               x_out=x_out, n_out=n_out, stream=s_)
+
+        lay.forward(n, stream=s, with_stats=with_stats, combine=combine)
+        return x_out, n_out

@@ -1,0 +1,145 @@
+"""A whole block as it is used: pre-norm, router with groups and a bias, 8-bit experts, shared
+expert, combine with post-norm, gate, residual and the next norm; each stage against the float64
+reference of what the GPU gave it (a rounding that flips in one stage then stays there)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_ops as B
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+T, D, E, K, F, FS = 300, 256, 16, 4, 144, 128
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
+def _block(dispatch, capacity=-1, shared=True, overlap=True):
+    from routing_dispatch_expert_moe_b200 import moe as M
+    from routing_dispatch_expert_moe_b200.layer import MoEBlock, MoELayer, MoEWeights
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    bf = torch.bfloat16
+    w = MoEWeights(Wg=rnd(D, E) * 0.1, W_gu=None, W_dn=None, select_bias=rnd(E) * 0.05,
+                   W_gu_i8=M.quantize_experts_i8(rnd(E, 2 * F, D) * 0.08),
+                   W_dn_i8=M.quantize_experts_i8((rnd(E, D, F) * 0.08).to(bf)))
+    if shared:
+        w.W_gu_s, w.W_dn_s = (rnd(1, 2 * FS, D) * 0.05).to(bf), (rnd(1, D, FS) * 0.05).to(bf)
+    lay = MoELayer(w, K, T, "sigmoid", True, 2.0, capacity, rows_dtype=bf, out_dtype=bf, dispatch=dispatch,
+                   overlap=overlap, n_groups=4, groups_kept=2)
+    blk = MoEBlock(lay, 1 + 0.1 * rnd(D), 1 + 0.1 * rnd(D), rnd(3, D), 0.5, 1 + 0.1 * rnd(D))
+    r = rnd(T, D).to(bf)
+    return M, w, lay, blk, r
+
+
+def _n(t):
+    return t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dispatch", ["permute", "gather"])
+@pytest.mark.parametrize("capacity", [-1, 60])
+def test_stages(dispatch, capacity):
+    M, w, lay, blk, r = _block(dispatch, capacity)
+    x, nn = blk.forward(r)
+    torch.cuda.synchronize()
+    assert M.moe_get_device_error() == 0
+    # the pre-norm
+    _, want = B.block_norm(_n(r), pre=_n(blk.pre_weight))
+    n = blk.n[:T]
+    assert (np.abs(_n(n) - want) <= (2.0 ** -8 + 64 * U) * np.abs(want)).all()
+    # routing of the GPU's own logits
+    idx, gate, margin = B.route_grouped(lay.logits.cpu().numpy(), K, 4, 2, "top2", "sigmoid", True, 2.0,
+                                        w.select_bias.cpu().numpy())
+    sure = margin > 1e-13
+    assert sure.all() and np.array_equal(lay.topk_idx.cpu().numpy(), idx)
+    assert (np.abs(_n(lay.topk_gate) - gate) <= 2 * U * gate).all()
+    # dispatch and 8 bits
+    off, row_of, tok = (t.cpu().numpy() for t in (lay.offsets, lay.row_of, lay.token_of_row))
+    used = int(off[-1])
+    q, s = B.quantize_rows(n.float().cpu().numpy())
+    if dispatch == "permute":
+        assert np.array_equal(lay.x_q.cpu().numpy()[:used], q[tok[:used]])
+        assert np.array_equal(lay.x_scale.cpu().numpy()[:used], s[tok[:used]])
+    else:
+        assert np.array_equal(lay.x_q.cpu().numpy()[:T], q) and np.array_equal(lay.x_scale.cpu().numpy()[:T], s)
+    if capacity > 0:
+        assert used < T * K                                   # something was dropped
+    # the expert products
+    wh = B.gate_up_i8(q[tok[:used]], s[tok[:used]], off, *(t.cpu().numpy() for t in w.W_gu_i8))
+    h = lay.h[:used]
+    assert (np.abs(_n(h) - wh) <= np.abs(wh) * (2.0 ** -8 + 2.0 ** -17) + 1e-30).all()
+    hq, hs = B.quantize_rows(h.float().cpu().numpy())
+    assert np.array_equal(lay.h_q.cpu().numpy()[:used], hq)
+    wy = B.down_i8(hq, hs, off, *(t.cpu().numpy() for t in w.W_dn_i8), lay.gate_of_row.cpu().numpy()[:used])
+    assert (np.abs(_n(lay.y_perm[:used]) - wy) <= np.abs(wy) * (2.0 ** -8 + 5 * U)).all()
+    # combine, post-norm, gate, residual, next norm: of the GPU's rows
+    rows = np.zeros((T * K, D))
+    rows[:used] = _n(lay.y_perm[:used])
+    y = B.combine_sum(rows, row_of, None, _n(lay.y_s[:T]))
+    wx, wn = B.block_norm(_n(r), y, _n(blk.post_weight), _n(blk.gate), 0.5, _n(blk.next_weight))
+    ysum = B.combine_sum(np.abs(rows), row_of, None, np.abs(_n(lay.y_s[:T])))
+    rms = np.sqrt((y * y).mean(1, keepdims=True))
+    spread = np.sqrt((ysum * ysum).mean(1, keepdims=True)) / rms
+    pg = np.abs(_n(blk.post_weight)) * np.repeat(np.abs(_n(blk.gate)), T // 3, axis=0)
+    size = 0.5 * np.abs(_n(r)) + pg * (ysum + np.abs(y) * spread) / rms
+    assert (np.abs(_n(x) - wx) <= 80 * U * size + 2.0 ** -8 * np.abs(wx)).all()
+    rx = np.sqrt((wx * wx).mean(1, keepdims=True))
+    total = np.sqrt((size * size).mean(1, keepdims=True)) / rx
+    tol = np.abs(_n(blk.next_weight)) * (size + np.abs(wx) * total) / rx
+    assert (np.abs(_n(nn) - wn) <= 110 * U * tol + 2.0 ** -8 * np.abs(wn)).all()
+
+
+def test_dispatch_forms_agree_and_a_chain_skips_the_norm():
+    M, w, lay, blk, r = _block("permute")
+    a, an = (t.clone() for t in blk.forward(r))
+    M2, w2, lay2, blk2, r2 = _block("gather")
+    b, bn = (t.clone() for t in blk2.forward(r2))
+    # both dispatch forms take weight-major tiles here (75 rows an expert): the same products
+    assert torch.equal(a, b) and torch.equal(an, bn)
+    # a second block fed with the first one's n' equals one that norms x' itself, but for that norm's
+    # rounding of x' (bf16): the n' given is closer to the truth; it only has to run and be finite
+    x2, n2 = blk.forward(a, n=an)
+    assert torch.isfinite(x2).all() and torch.isfinite(n2).all()
+    assert M.moe_get_device_error() == 0
+
+
+@pytest.mark.parametrize("overlap", [True, False])
+def test_smaller_batches_streams_and_graph(overlap):
+    M, w, lay, blk, r = _block("permute", overlap=overlap)
+    want = {}
+    for t in (3, 30, 300):
+        x, n = blk.forward(r[:t])
+        want[t] = (x.clone(), n.clone())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    x, n = blk.forward(r[:30], stream=s)
+    s.synchronize()
+    assert torch.equal(x, want[30][0]) and torch.equal(n, want[30][1])
+    buf = torch.zeros_like(r[:300])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            x, n = blk.forward(buf, stream=side)
+    buf.copy_(r)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(x, want[300][0]) and torch.equal(n, want[300][1])
+    assert M.moe_get_device_error() == 0
+
+
+def test_launch_count():
+    _, _, lay, _, _ = _block("permute", shared=False)
+    _, _, lay2, _, _ = _block("gather", shared=False)
+    # router, grouped top-k, rank, scatter, x to 8 bits, gate/up, h to 8 bits, down, combine
+    assert lay.launches_per_forward(False) == 9 and lay2.launches_per_forward(False) == 9
