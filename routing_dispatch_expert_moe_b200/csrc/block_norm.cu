@@ -271,7 +271,7 @@ __device__ __forceinline__ void bulk_row(uint32_t dst, const void* src, uint32_t
 // barrier of that row's first reduction), or, with one buffer, past the row itself.
 // gate * post of the current gate group waits in shared memory (each thread its own columns).
 template <typename YT, typename RT, typename NT, int V>
-__global__ void __launch_bounds__(V == 1 ? 256 : 512, V == 1 ? 3 : 1)
+__global__ void __launch_bounds__(V == 1 ? 64 : 512, V == 1 ? 12 : 1)
 block_norm_grad_kernel(const NormGradArgs a) {
   extern __shared__ __align__(16) uint8_t nsm[];
   __shared__ float2 part[2][2][kNormMaxWarps];
@@ -567,6 +567,15 @@ Shape row_shape(int n8) {
   return s;
 }
 
+// The backward pass: two vectors a thread from 64 on, so that a row's two reductions are shared by
+// half the warps (d = 2048: 54 us against 62 with one).
+Shape grad_shape(int n8) {
+  Shape s;
+  s.V = n8 <= 64 ? 1 : 2;
+  s.threads = ((n8 + s.V - 1) / s.V + 31) / 32 * 32;
+  return s;
+}
+
 template <typename YT, typename RT, typename NT, bool COMBINE>
 moe_status run_norm(const NormArgs& a, cudaStream_t s) {
   const Shape sh = row_shape(a.d / 8);
@@ -586,17 +595,16 @@ moe_status norm_types(const NormArgs& a, int r_dtype, int n_dtype, cudaStream_t 
                             : run_norm<YT, __nv_bfloat16, __nv_bfloat16, COMBINE>(a, s);
 }
 
-// Blocks of the backward pass: what the device holds at once (a multiprocessor: three of 256
-// threads and one vector each, 512 threads of two, up to 16 small ones), at most one a token.
+// Blocks of the backward pass: what the device holds at once (a multiprocessor: 512 threads of
+// two vectors each, or up to 12 small blocks of one), at most one a token.
 struct GradPlan {
   int blocks, per_sm;
 };
 GradPlan grad_plan(int T, int d) {
   GradPlan p;
-  const Shape sh = row_shape(d / 8);
-  p.per_sm = (sh.V == 1 ? 768 : 512) / sh.threads;
-  if (p.per_sm < 1) p.per_sm = 1;
-  if (p.per_sm > 16) p.per_sm = 16;
+  const Shape sh = grad_shape(d / 8);
+  p.per_sm = (sh.V == 1 ? 768 : 512) / sh.threads;         // at least 1
+  if (p.per_sm > 12) p.per_sm = 12;
   const int want = p.per_sm * num_sms();
   p.blocks = T < want ? T : want;
   return p;
@@ -621,7 +629,7 @@ moe_status run_grad_v(NormGradArgs a, const GradPlan& p, int threads, cudaStream
 
 template <typename YT, typename RT, typename NT>
 moe_status run_grad(const NormGradArgs& a, const GradPlan& p, cudaStream_t s) {
-  const Shape sh = row_shape(a.d / 8);
+  const Shape sh = grad_shape(a.d / 8);
   if (sh.V == 1) return run_grad_v<YT, RT, NT, 1>(a, p, sh.threads, s);
   return run_grad_v<YT, RT, NT, 2>(a, p, sh.threads, s);
 }

@@ -13,7 +13,7 @@
 // What it costs.  A token reads 4E bytes once and writes 8k; the work is the E scores, the two
 // selections and the k gates, so at hundreds of experts it is bound by instruction issue.
 //   - One warp per token.  A group belongs to a team of 32 / G' lanes (G' = G rounded up to a
-//     power of two), so a lane finds the two largest keys of its part in registers and a few
+//     power of two), so a lane finds the two largest keys of its part and a few
 //     shuffles finish the group.
 //   - The selection runs on fp32 keys a with a known bound |a - key| <= delta.  The kept groups'
 //     keys are spread evenly over the lanes through shared memory; the k-th largest of the 32
@@ -30,7 +30,7 @@
 
 #include "common.cuh"
 #include "f32x2.cuh"
-#include "warp_rows.cuh"
+#include "tc_prims.cuh"
 
 namespace moe {
 namespace {
@@ -132,7 +132,7 @@ struct GroupArgs {
 // group (every team-th expert) in local memory and its best one at hand; k rounds of an arg-max
 // over the lanes follow.  One token here holds up its warp for some 15 us.
 template <int SCORE>
-__device__ __noinline__ Pick route_token_fp64(const GroupArgs& a, const float* l) {
+__device__ __noinline__ Pick route_token_fp64(const GroupArgs& a, const float* __restrict__ l) {
   const int lane = threadIdx.x & 31;
   const int L = a.team, g = lane / L, tl = lane - g * L;
   const bool in_g = g < a.G;
@@ -144,11 +144,11 @@ __device__ __noinline__ Pick route_token_fp64(const GroupArgs& a, const float* l
   out.z = 1.0;
   if (SCORE == MOE_SCORE_SOFTMAX) {
     double m = -INFINITY, z = 0.0;
-    for (int i = 0; i < count; ++i) m = fmax(m, (double)clean_logit(l[e0 + i * L]));
+    for (int i = 0; i < count; ++i) m = fmax(m, (double)clean_logit(__ldg(l + e0 + i * L)));
     m = wmax_d(m);
     if (m > -INFINITY) {
 #pragma unroll 2
-      for (int i = 0; i < count; ++i) z += exp((double)clean_logit(l[e0 + i * L]) - m);
+      for (int i = 0; i < count; ++i) z += exp((double)clean_logit(__ldg(l + e0 + i * L)) - m);
       z = wsum_d(z);
       out.m = m;
       out.z = z;
@@ -160,7 +160,7 @@ __device__ __noinline__ Pick route_token_fp64(const GroupArgs& a, const float* l
   int bi = -1;
 #pragma unroll 2
   for (int i = 0; i < count; ++i) {
-    const float lf = clean_logit(l[e0 + i * L]);
+    const float lf = clean_logit(__ldg(l + e0 + i * L));
     double k = (double)lf, v = k;
     if (scored && lf > -INFINITY) {
       v = SCORE == MOE_SCORE_SOFTMAX ? exp(k - out.m) / out.z : score64(k, SCORE);
@@ -208,27 +208,69 @@ __device__ __noinline__ Pick route_token_fp64(const GroupArgs& a, const float* l
   }
   out.s = 0.0;
   if (SCORE != MOE_SCORE_SOFTMAX && lane < a.k) {
-    const float lf = clean_logit(l[out.idx]);
+    const float lf = clean_logit(__ldg(l + out.idx));
     if (lf > -INFINITY) out.s = score64((double)lf, SCORE);
   }
   return out;
 }
 
-// The rank of this lane's group by exact values, when the fp32 ones are too close at the border.
-// `near` marks the lane's experts that may be among its group's two largest (by fp32 keys less
-// twice their error); only they are evaluated in fp64.  Not for softmax (its sum is not exact).
-template <int SCORE>
-__device__ __noinline__ int exact_rank(const GroupArgs& a, const float* l, unsigned long long near, bool vec) {
+// A row of keys in shared memory as a lane sees it: its part of its group, in `chunks` chunks of
+// four (VEC: four neighbouring experts).
+template <bool VEC>
+struct Part {
+  int base, n, L, tl, chunks;
+  bool in_g;
+  __device__ __forceinline__ int place(int i) const { return VEC ? 4 * (tl + L * (i >> 2)) + (i & 3) : tl + L * i; }
+  __device__ __forceinline__ bool have(int i) const { return in_g && place(i) < n; }
+  // chunk c of p (global or shared), `none` where it does not exist
+  __device__ __forceinline__ void get(const float* p, int c, float (&f)[4], float none) const {
+    if constexpr (VEC) {
+      float4 q = make_float4(none, none, none, none);
+      if (have(4 * c)) q = *reinterpret_cast<const float4*>(p + base + place(4 * c));
+      f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = have(4 * c + k) ? p[base + place(4 * c + k)] : none;
+    }
+  }
+  __device__ __forceinline__ void put(float* p, int c, const float (&f)[4]) const {
+    if constexpr (VEC) {
+      if (have(4 * c)) *reinterpret_cast<float4*>(p + base + place(4 * c)) = make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (have(4 * c + k)) p[base + place(4 * c + k)] = f[k];
+    }
+  }
+};
+
+// The rank of this lane's group by exact values, when the fp32 ones are too close at the border:
+// only the experts whose fp32 key is at least th (their group's second largest, or its largest,
+// less twice the error) are evaluated in fp64.  Not for softmax (its sum is not exact).
+template <bool VEC, int SCORE>
+__device__ __noinline__ int exact_rank(const GroupArgs& a, const Part<VEC>& part, const float* l, const float* row,
+                                       float th) {
   const int lane = threadIdx.x & 31;
-  const int L = a.team, g = lane / L, tl = lane - g * L;
+  const int L = a.team, g = lane / L;
   double v1 = -INFINITY, v2 = -INFINITY;
-  while (near) {
-    const int i = __ffsll((long long)near) - 1;
-    near &= near - 1;
-    const int e = g * a.n + (vec ? 4 * (tl + L * (i >> 2)) + (i & 3) : tl + L * i);
-    double v = score64((double)clean_logit(l[e]), SCORE);
-    if (a.bias) v += (double)__ldg(a.bias + e);
-    if (v > v1) { v2 = v1; v1 = v; } else if (v > v2) v2 = v;
+  for (int c = 0; c < part.chunks; ++c) {
+    float key[4];
+    part.get(row, c, key, -INFINITY);
+    if (!a.bias) {                                         // the row holds logits, not scores
+      const float2 x = score32<SCORE>(clean_logit(key[0]), clean_logit(key[1]));
+      const float2 y = score32<SCORE>(clean_logit(key[2]), clean_logit(key[3]));
+      const float s[4] = {x.x, x.y, y.x, y.y};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) key[k] = key[k] > -INFINITY ? s[k] : -INFINITY;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!(key[k] > -INFINITY && key[k] >= th)) continue;
+      const int e = part.base + part.place(4 * c + k);
+      double v = score64((double)clean_logit(__ldg(l + e)), SCORE);
+      if (a.bias) v += (double)__ldg(a.bias + e);
+      if (v > v1) { v2 = v1; v1 = v; } else if (v > v2) v2 = v;
+    }
   }
   __syncwarp();
   for (int o = 1; o < L; o <<= 1) {
@@ -260,43 +302,57 @@ __device__ __forceinline__ float kth_of_lanes(float v, int kth) {
   return __shfl_sync(kFull, v, kth - 1);
 }
 
+// Floats as integers of the same order (-0 as +0; never 0), and back.
+__device__ __forceinline__ unsigned ordered32(float v) {
+  const unsigned u = __float_as_uint(v + 0.f);
+  return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered32(unsigned o) {
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
 // Doubles as integers of the same order (-0 as +0).
 __device__ __forceinline__ unsigned long long ordered(double v) {
   const long long b = __double_as_longlong(v + 0.0);
   return (unsigned long long)b ^ ((unsigned long long)(b >> 63) | 0x8000000000000000ull);
 }
 
-// EPL: keys a lane can hold of its group's part, in chunks of four (VEC: four consecutive
-// experts, one load); a.chunks of them are used.
-template <int EPL, bool VEC, int SCORE>
-__global__ void __launch_bounds__(32 * kGroupWarps, EPL <= 32 ? 3 : 2)
+// VEC: groups of whole 16-byte pieces; a warp's row comes by one bulk copy, asked for as soon as the
+// token before has its candidates.  The row stays in shared memory, where the keys replace the
+// logits (a bias given), so that the kernel needs few registers, whatever n, and 32 warps hide its
+// chains of shuffles and fp64.  32768 tokens, 896 experts in 16 groups, k = 16: 63 us by logit,
+// 110 us for the two best of sqrt(softplus) + bias, where the 18 us of HBM time stand against some
+// 2400 instructions a token; 71 us with all groups kept (keys in registers, 24 warps: 75, 106, 124).
+template <bool VEC, int SCORE>
+__global__ void __launch_bounds__(32 * kGroupWarps, 4)
 route_group_kernel(const __grid_constant__ GroupArgs a) {
   extern __shared__ __align__(16) float gsm[];
-  __shared__ __align__(8) uint64_t s_bar[kGroupWarps][2];
+  __shared__ __align__(8) uint64_t s_bar[kGroupWarps];
   __shared__ int s_abort;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int E = a.E, n = a.n, k = a.k, L = a.team;
-  const int pool = a.kept * n;                             // experts of the kept groups
-  const int keys_pitch = (pool + 3) / 4 * 4;
-  float* keys = gsm + (size_t)w * (keys_pitch + (VEC ? 2 * E : 0));   // their fp32 keys, group by group
-  volatile int* abort_flag = &s_abort;
-  if (threadIdx.x == 0) s_abort = 0;
-  __syncthreads();
-  WarpRows rows;                                           // VEC: the rows of logits, one ahead
-  if (VEC) rows.init(s_bar[w], reinterpret_cast<uint8_t*>(keys + keys_pitch), (uint32_t)E * 4, lane);
   __shared__ int s_group[kGroupWarps][32];                 // the kept groups, ascending
   __shared__ int s_cand[kGroupWarps][32];
   __shared__ double s_score[kGroupWarps][32];
-  const int g = lane / L, tl = lane - g * L;               // this lane's group, its place in the team
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int E = a.E, n = a.n, k = a.k, L = a.team;
+  const int shift = __ffs(L) - 1;                          // lanes to groups: L is a power of two
+  const float inv_n = 1.f / (float)n;
+  const int pool = a.kept * n;                             // experts of the kept groups
+  float* row = gsm + (size_t)w * ((E + 3) / 4 * 4);
+  volatile int* abort_flag = &s_abort;
+  const uint32_t bar = smem_u32(&s_bar[w]);
+  if (threadIdx.x == 0) s_abort = 0;
+  if (VEC && lane == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int g = lane >> shift, tl = lane & (L - 1);        // this lane's group, its place in the team
   const bool in_g = g < a.G;
+  const Part<VEC> part{g * n, n, L, tl, a.chunks, in_g};
   const bool biased = a.bias != nullptr;
   const bool by_logit = !biased && !a.top2;                // fp32 keys are exact
   const bool need_z = SCORE == MOE_SCORE_SOFTMAX && (!by_logit || !a.renorm);
-  // expert i of the lane's part, and whether it exists (a chunk of VEC exists as a whole)
-  auto place = [&](int i) { return VEC ? 4 * (tl + L * (i >> 2)) + (i & 3) : tl + L * i; };
-  auto have = [&](int i) { return in_g && place(VEC ? i & ~3 : i) < n; };
   float bmax = 0.f;                                        // largest |bias|: part of the bound
-  bool odd = false;                                        // a NaN bias: every token in fp64
+  bool odd = false;                                        // a NaN or infinite bias: every token in fp64
   if (biased)
     for (int e = lane; e < E; e += 32) {
       const float b = fabsf(__ldg(a.bias + e));
@@ -307,71 +363,86 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
   odd = __any_sync(kFull, odd);
   const long long nw = (long long)gridDim.x * warps;
   const long long first = (long long)blockIdx.x * warps + w;
-  unsigned it = 0, loaded = 0;                             // tokens done; rows asked for
-  if (VEC && lane == 0 && first < a.T) rows.load(loaded++, a.logits + first * E);
-  for (long long t = first; t < a.T; t += nw, ++it) {
+  auto ask = [&](const float* src) {                       // lane 0: a row into the buffer
+    mbar_expect_tx(bar, (uint32_t)E * 4);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(row)),
+                 "l"(src), "r"((uint32_t)E * 4), "r"(bar)
+                 : "memory");
+  };
+  if (VEC && lane == 0 && first < a.T) ask(a.logits + first * E);
+  uint32_t parity = 0;
+  for (long long t = first; t < a.T; t += nw) {
     const float* l = a.logits + t * E;
-    // -------------------------------------------------- logits and fp32 keys
     if constexpr (VEC) {
-      if (!rows.wait(it, abort_flag, a.err)) break;
-      l = rows.row(it);
-      __syncwarp();                                        // every lane is done with the other buffer
-      if (lane == 0 && t + nw < a.T) rows.load(loaded++, a.logits + (t + nw) * E);
-    }
-    float v[EPL];
-    auto fetch = [&](const float* p, int i, float (&f)[4], float none) {
-      if constexpr (VEC) {
-        float4 q = make_float4(none, none, none, none);
-        if (have(i)) q = *reinterpret_cast<const float4*>(p + g * n + place(i));
-        f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) f[c] = have(i + c) ? __ldg(p + g * n + place(i + c)) : none;
+      const bool got = mbar_wait(bar, parity, abort_flag, a.err);
+      if (!__all_sync(kFull, got)) {
+        if (lane == 0) mbar_wait_drain(bar, parity, a.err);   // the copy lands before the block ends
+        break;
       }
-    };
-#pragma unroll
-    for (int i = 0; i < EPL; i += 4) {
-      float f[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (i < 4 * a.chunks) fetch(l, i, f, -INFINITY);     // uniform
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[i + c] = f[c];
+      parity ^= 1u;
+    } else {
+      __syncwarp();                                        // the previous token's row is read
+      for (int e = lane; e < E; e += 32) row[e] = __ldg(l + e);
+      __syncwarp();
     }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if ((i & ~3) < 4 * a.chunks) v[i] = clean_logit(v[i]);
+    // -------------------------------------------------- fp32 keys, the groups' two largest
     float m = -INFINITY, z = 0.f, delta = 0.f;
     if (need_z || !by_logit) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if ((i & ~3) < 4 * a.chunks) m = fmaxf(m, v[i]);
-      m = wmax(m);
-    }
-    if (need_z && m > -INFINITY) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if ((i & ~3) < 4 * a.chunks) z += expf(v[i] - m);
-      z = wsum(z);
+#pragma unroll 4
+      for (int c = 0; c < a.chunks; ++c) {
+        float f[4];
+        part.get(row, c, f, -INFINITY);
+        m = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), m);   // drops NaNs
+      }
+      m = fminf(wmax(m), FLT_MAX);
     }
     const bool dead = need_z && !(m > -INFINITY);          // every expert masked
+    if (need_z && !dead) {
+#pragma unroll 2
+      for (int c = 0; c < a.chunks; ++c) {
+        float f[4];
+        part.get(row, c, f, -INFINITY);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z += expf(clean_logit(f[i]) - m);
+      }
+      z = wsum(z);
+    }
     bool slow = odd;
-    if (!by_logit) {
-      const float iz = __fdividef(1.f, z);
-      auto score_of = [&](float x, float y) {
-        if (SCORE == MOE_SCORE_SOFTMAX) return make_float2(__expf(x - m) * iz, __expf(y - m) * iz);
-        return score32<SCORE>(x, y);
-      };
-#pragma unroll
-      for (int i = 0; i < EPL; i += 4) {
-        if (i >= 4 * a.chunks) continue;                   // uniform
-        float b[4] = {0.f, 0.f, 0.f, 0.f};
-        if (biased) fetch(a.bias, i, b, 0.f);
-#pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-          const float2 s = score_of(v[i + c], v[i + c + 1]);
-          const float2 key = unpack2(add2(pack2(s.x, s.y), pack2(b[c], b[c + 1])));
-          v[i + c] = v[i + c] > -INFINITY ? key.x : -INFINITY;
-          v[i + c + 1] = v[i + c + 1] > -INFINITY ? key.y : -INFINITY;
+    const float iz = need_z ? __fdividef(1.f, z) : 0.f;
+    auto score_of = [&](float x, float y) {
+      if (SCORE == MOE_SCORE_SOFTMAX) return make_float2(__expf(x - m) * iz, __expf(y - m) * iz);
+      return score32<SCORE>(x, y);
+    };
+    float g1 = -INFINITY, g2 = -INFINITY;
+    if (by_logit) {
+      if (a.kept < a.G) {
+#pragma unroll 4
+        for (int c = 0; c < a.chunks; ++c) {
+          float f[4];
+          part.get(row, c, f, -INFINITY);
+          g1 = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), g1);
         }
+        g1 = fminf(g1, FLT_MAX);
+      }
+    } else {
+#pragma unroll 2
+      for (int c = 0; c < a.chunks; ++c) {
+        float f[4], b[4] = {0.f, 0.f, 0.f, 0.f};
+        part.get(row, c, f, -INFINITY);
+        if (biased) part.get(a.bias, c, b, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float x = clean_logit(f[i]), y = clean_logit(f[i + 1]);
+          const float2 s = score_of(x, y);
+          const float2 key = unpack2(add2(pack2(s.x, s.y), pack2(b[i], b[i + 1])));
+          f[i] = x > -INFINITY ? key.x : -INFINITY;
+          f[i + 1] = y > -INFINITY ? key.y : -INFINITY;
+          const float hi = fmaxf(f[i], f[i + 1]), lo = fminf(f[i], f[i + 1]);
+          g2 = fmaxf(fmaxf(g2, lo), fminf(g1, hi));
+          g1 = fmaxf(g1, hi);
+        }
+        if (biased) part.put(row, c, f);
       }
       // the scores' error relative to the largest one, the largest logit's (see score32; softmax:
       // the sum and its reciprocal instead), and one rounding of s + b
@@ -381,72 +452,50 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
       slow |= !(smax > 1e-12f);                            // near the flushed subnormals
     }
     // -------------------------------------------------- groups
-    float g1 = -INFINITY, g2 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      if ((i & ~3) >= 4 * a.chunks) continue;
-      g2 = fmaxf(g2, fminf(g1, v[i]));
-      g1 = fmaxf(g1, v[i]);
-    }
-    for (int o = 1; o < L; o <<= 1) {
-      const float c1 = __shfl_xor_sync(kFull, g1, o), c2 = __shfl_xor_sync(kFull, g2, o);
-      g2 = fmaxf(fminf(g1, c1), fmaxf(g2, c2));
-      g1 = fmaxf(g1, c1);
-    }
     bool keep = in_g;
     if (a.kept < a.G) {
-      const float gv = a.top2 && g2 > -INFINITY ? g1 + g2 : g1;
-      int rank = 0;
-      for (int o = 0; o < a.G; ++o) {
-        const float c = __shfl_sync(kFull, gv, o * L);
-        rank += c > gv || (c == gv && o < g);
+      for (int o = 1; o < L; o <<= 1) {
+        const float c1 = __shfl_xor_sync(kFull, g1, o), c2 = __shfl_xor_sync(kFull, g2, o);
+        g2 = fmaxf(fminf(g1, c1), fmaxf(g2, c2));
+        g1 = fmaxf(g1, c1);
       }
-      keep = in_g && rank < a.kept;
+      // the kept groups, one warp maximum each: a value as an integer of its order, of equal ones
+      // the lower group
+      const float gv = a.top2 && g2 > -INFINITY ? g1 + g2 : g1;
+      unsigned left = in_g ? ordered32(gv) : 0u, worst = 0u;   // no value's integer is 0
+      keep = false;
+      for (int j = 0; j < a.kept; ++j) {
+        worst = __reduce_max_sync(kFull, left);
+        const int best_g = (__ffs(__ballot_sync(kFull, left == worst)) - 1) >> shift;
+        if (g == best_g) {
+          keep = true;
+          left = 0u;
+        }
+      }
       if (!by_logit) {                                     // the border must be wider than the error
-        const float lo = wmax(keep ? -gv : -INFINITY), hi = wmax(in_g && !keep ? gv : -INFINITY);
-        if (!(-lo - hi > 6.f * delta + 2.4e-7f * (fabsf(lo) + fabsf(hi))) && hi > -INFINITY) {
-          if (SCORE == MOE_SCORE_SOFTMAX) {
+        const float lo = from_ordered32(worst), hi = from_ordered32(__reduce_max_sync(kFull, left));
+        if (!(lo - hi > 6.f * delta + 2.4e-7f * (fabsf(lo) + fabsf(hi))) && hi > -INFINITY) {
+          if (SCORE == MOE_SCORE_SOFTMAX)
             slow = true;
-          } else {
-            const float th = (a.top2 ? g2 : g1) - 2.f * delta;
-            unsigned long long near = 0;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-              if (v[i] > -INFINITY && v[i] >= th) near |= 1ull << i;
-            keep = exact_rank<SCORE>(a, l, near, VEC) < a.kept && in_g;
-          }
+          else
+            keep = exact_rank<VEC, SCORE>(a, part, l, row, (a.top2 ? g2 : g1) - 2.f * delta) < a.kept && in_g;
         }
       }
     }
     const unsigned heads = __ballot_sync(kFull, keep && tl == 0);
-    const int order = __popc(heads & ((1u << (g * L)) - 1u));   // this group's place among the kept
-    // -------------------------------------------------- the kept groups' keys, spread evenly
-    const bool again = a.top2 && !biased;                  // groups by scores, experts by logit
-    if (again) delta = 0.f;
-    __syncwarp();                                          // the previous token's keys are read
-    if (keep) {
-      if (tl == 0) s_group[w][order] = g;
-#pragma unroll
-      for (int i = 0; i < EPL; i += 4) {
-        if (i >= 4 * a.chunks) continue;
-        float f[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
-        if (again) {
-          fetch(l, i, f, -INFINITY);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) f[c] = clean_logit(f[c]);
-        }
-        if constexpr (VEC) {
-          if (have(i)) *reinterpret_cast<float4*>(keys + order * n + place(i)) = make_float4(f[0], f[1], f[2], f[3]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (have(i + c)) keys[order * n + place(i + c)] = f[c];
-        }
-      }
-    }
-    __syncwarp();
+    if (keep && tl == 0) s_group[w][__popc(heads & ((1u << lane) - 1u))] = g;
+    if (!biased) delta = 0.f;                              // experts by logit, whatever the groups go by
+    __syncwarp();                                          // the keys and the groups are written
+    // -------------------------------------------------- candidates
+    // expert number p of the kept groups (p / n by a product: p < 1024, half a step is far off)
+    auto expert = [&](int p) {
+      if (a.kept == a.G) return p;
+      const int o = (int)(((float)p + 0.5f) * inv_n);
+      return s_group[w][o] * n + (p - o * n);
+    };
     float best = -INFINITY;
-    for (int p = lane; p < pool; p += 32) best = fmaxf(best, keys[p]);
+    for (int p = lane; p < pool; p += 32) best = fmaxf(best, row[expert(p)]);
+    best = fminf(best, FLT_MAX);
     float tau = kth_of_lanes(best, k);
     // the keys not below the threshold, in index order; the first 32 get a lane each
     auto compact = [&]() {
@@ -454,10 +503,11 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
       int c = 0;
       for (int p0 = 0; p0 < pool; p0 += 32) {
         const int p = p0 + lane;
-        const bool in = p < pool && keys[p] >= th;
+        const int e = p < pool ? expert(p) : 0;
+        const bool in = p < pool && row[e] >= th;
         const unsigned b = __ballot_sync(kFull, in);
         const int at = c + __popc(b & ((1u << lane) - 1u));
-        if (in && at < 32) s_cand[w][at] = p;
+        if (in && at < 32) s_cand[w][at] = e;
         c += __popc(b);
       }
       return c;
@@ -470,7 +520,7 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
       for (int it = 0; it < 24; ++it) {
         const float mid = 0.5f * lo + 0.5f * hi;
         int above = 0;
-        for (int p = lane; p < pool; p += 32) above += keys[p] >= mid;
+        for (int p = lane; p < pool; p += 32) above += row[expert(p)] >= mid;
         above = (int)__reduce_add_sync(kFull, (unsigned)above);
         if (above >= k) lo = mid; else hi = mid;
         if (above >= k && above <= 32) break;
@@ -481,6 +531,14 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
     }
     __syncwarp();
     slow = slow || !(tau > -INFINITY) || c > 32 || c < k;
+    int e = 0;
+    float af = 0.f;
+    if (lane < c && lane < 32) {
+      e = s_cand[w][lane];
+      af = row[e];
+    }
+    __syncwarp();                                          // the row is done with
+    if (VEC && lane == 0 && t + nw < a.T) ask(l + nw * E);
     // -------------------------------------------------- exact order of what is left
     Pick pick;
     pick.idx = 0;
@@ -488,15 +546,9 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
     pick.z = (double)z;
     pick.s = 0.0;
     if (!slow) {
-      int e = 0;
       double key = -INFINITY, s = 0.0;
-      float af = 0.f;
       if (lane < c) {
-        const int p = s_cand[w][lane];
-        const int o = p / n;
-        e = s_group[w][o] * n + (p - o * n);
-        af = keys[p];
-        const double lf = (double)clean_logit(l[e]);
+        const double lf = (double)clean_logit(biased ? __ldg(l + e) : af);
         if (SCORE != MOE_SCORE_SOFTMAX) s = score64(lf, SCORE);
         key = !biased ? lf : SCORE == MOE_SCORE_SOFTMAX ? (double)af : s + (double)__ldg(a.bias + e);
       }
@@ -535,7 +587,7 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
     // -------------------------------------------------- gates (fp64, rounded once)
     double s = 0.0;
     if (SCORE == MOE_SCORE_SOFTMAX) {
-      const float lf = lane < k ? clean_logit(l[pick.idx]) : -INFINITY;
+      const float lf = lane < k ? clean_logit(__ldg(l + pick.idx)) : -INFINITY;
       const double mm = a.renorm ? (double)wmax(lf) : pick.m;
       if (lf > -INFINITY) s = exp((double)lf - mm);
       if (!a.renorm) s /= pick.z;
@@ -550,38 +602,22 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
       a.topk_idx[t * k + lane] = pick.idx;
       a.topk_gate[t * k + lane] = (float)(s * (double)a.scale);
     }
+    __syncwarp();                                          // the candidates' lists are read
   }
-  if (VEC && lane == 0) rows.drain(it, loaded, a.err);     // after a timeout: what is still in flight
 }
 
 // Warps a block: eight, or fewer where the tokens would leave multiprocessors without any.
-template <int EPL, bool VEC, int SCORE>
+template <bool VEC, int SCORE>
 moe_status run_group(const GroupArgs& a, cudaStream_t s) {
   const int sms = num_sms();
   int warps = (a.T + sms - 1) / sms;
   if (warps > kGroupWarps) warps = kGroupWarps;
-  constexpr size_t kMost = (size_t)kGroupWarps * 3 * 4096; // three rows of 1024 a warp
-  static std::atomic<int> configured[kMaxDevices];
-  const moe_status st = ensure_smem_limit(configured, route_group_kernel<EPL, VEC, SCORE>, kMost);
-  if (st != MOE_OK) return st;
-  const size_t smem = (size_t)warps * ((a.kept * a.n + 3) / 4 * 4 + (VEC ? 2 * a.E : 0)) * sizeof(float);
+  const size_t smem = (size_t)warps * ((a.E + 3) / 4 * 4) * sizeof(float);   // at most 32 KB
   long long blocks = ((long long)a.T + warps - 1) / warps;
-  const long long cap = (long long)sms * 3;
+  const long long cap = (long long)sms * 4;
   if (blocks > cap) blocks = cap;
-  route_group_kernel<EPL, VEC, SCORE><<<(unsigned)blocks, 32 * warps, smem, s>>>(a);
+  route_group_kernel<VEC, SCORE><<<(unsigned)blocks, 32 * warps, smem, s>>>(a);
   return check_launch();
-}
-
-template <int SCORE>
-moe_status dispatch_group(const GroupArgs& a, bool vec, cudaStream_t s) {
-  if (vec) {
-    if (a.chunks <= 2) return run_group<8, true, SCORE>(a, s);
-    if (a.chunks <= 8) return run_group<32, true, SCORE>(a, s);
-    return run_group<64, true, SCORE>(a, s);
-  }
-  if (a.chunks <= 2) return run_group<8, false, SCORE>(a, s);
-  if (a.chunks <= 8) return run_group<32, false, SCORE>(a, s);
-  return run_group<64, false, SCORE>(a, s);
 }
 
 }  // namespace
@@ -595,10 +631,12 @@ moe_status launch_route_grouped(const float* logits, int T, int E, int k, int n_
   while (p2 < n_groups) p2 <<= 1;
   a.team = 32 / p2;
   const bool vec = a.n % 4 == 0 && aligned16(logits) && aligned16(bias);
-  a.chunks = (a.n + 4 * a.team - 1) / (4 * a.team);        // at most 16: n <= 1024 / G, G > p2 / 2
-  if (score == MOE_SCORE_SOFTMAX) return dispatch_group<MOE_SCORE_SOFTMAX>(a, vec, s);
-  if (score == MOE_SCORE_SIGMOID) return dispatch_group<MOE_SCORE_SIGMOID>(a, vec, s);
-  return dispatch_group<MOE_SCORE_SQRT_SOFTPLUS>(a, vec, s);
+  a.chunks = (a.n + 4 * a.team - 1) / (4 * a.team);
+  if (score == MOE_SCORE_SOFTMAX)
+    return vec ? run_group<true, MOE_SCORE_SOFTMAX>(a, s) : run_group<false, MOE_SCORE_SOFTMAX>(a, s);
+  if (score == MOE_SCORE_SIGMOID)
+    return vec ? run_group<true, MOE_SCORE_SIGMOID>(a, s) : run_group<false, MOE_SCORE_SIGMOID>(a, s);
+  return vec ? run_group<true, MOE_SCORE_SQRT_SOFTPLUS>(a, s) : run_group<false, MOE_SCORE_SQRT_SOFTPLUS>(a, s);
 }
 
 }  // namespace moe
