@@ -8,6 +8,7 @@ or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -680,31 +681,25 @@ def moe_router_stats(logits, counts, kept, k: int, score: str = "softmax", load=
 
 
 # ---------------------------------------------------------------- groups, 8-bit experts, block norms
-class _on:
-    """Makes the device of `t` current for a call, and checks that the other tensors are on it."""
+def _run(name: str, stream, tensors, *args):
+    """Calls entry point `name` with args and the stream's handle, on the device that every tensor
+    (None left out) is on; that device is made current for the call where it is not.  The plain
+    case is kept short: the small calls are as long as their host side."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"every tensor of a call must be on one device: {t.device} beside {tensors[0].device}")
+    f = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == index:
+        status = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    if status != MOE_OK:
+        raise MoEError(name, status)
 
-    __slots__ = ("index", "back")
 
-    def __init__(self, t: torch.Tensor, *others):
-        self.index = t.get_device()
-        for o in others:
-            if o is not None and o.get_device() != self.index:
-                raise ValueError(f"every tensor of a call must be on one device: {o.device} beside {t.device}")
-
-    def __enter__(self):
-        self.back = torch.cuda.current_device()
-        if self.back != self.index:
-            torch.cuda.set_device(self.index)
-        return self
-
-    def __exit__(self, *exc):
-        if self.back != self.index:
-            torch.cuda.set_device(self.back)
-
-    def stream(self, given):
-        """The given stream's handle, or the current one's (read without building a Stream object,
-        which costs 3 us of a small call's 15)."""
-        return torch._C._cuda_getCurrentRawStream(self.index) if given is None else given.cuda_stream
+_HERE_ALREADY = contextlib.nullcontext()
 
 
 def _want(t: torch.Tensor, name: str, dtype, shape):
@@ -752,11 +747,9 @@ def moe_route_grouped(logits, k: int, n_groups: int, groups_kept: int, group_sco
         _want(topk_idx, "topk_idx", torch.int32, (T, k))
     topk_gate = _new((T, k), torch.float32, dev) if topk_gate is None else \
         _want(topk_gate, "topk_gate", torch.float32, (T, k))
-    with _on(logits, select_bias, topk_idx, topk_gate) as on:
-        _check("moe_route_grouped", lib().moe_route_grouped(
-            _ptr(logits), _ptr(select_bias), T, E, k, n_groups, groups_kept,
-            _choice(GROUP_SCORE, group_score, "group_score"), _choice(SCORE, score, "score"), 1 if renormalize else 0,
-            scale, _ptr(topk_idx), _ptr(topk_gate), on.stream(stream)))
+    _run("moe_route_grouped", stream, (logits, select_bias, topk_idx, topk_gate), _ptr(logits), _ptr(select_bias), T,
+         E, k, n_groups, groups_kept, _choice(GROUP_SCORE, group_score, "group_score"), _choice(SCORE, score,
+         "score"), 1 if renormalize else 0, scale, _ptr(topk_idx), _ptr(topk_gate))
     return topk_idx, topk_gate
 
 
@@ -778,10 +771,9 @@ def moe_route_backward(logits, topk_idx=None, d_gate=None, score: str = "softmax
     if load is not None:
         _want(load, "load", torch.float32, (E,))
     d_logits = torch.empty_like(logits) if d_logits is None else _want(d_logits, "d_logits", torch.float32, (T, E))
-    with _on(logits, topk_idx, d_gate, load, d_logits) as on:
-        _check("moe_route_backward", lib().moe_route_backward(
-            _ptr(logits), _ptr(topk_idx), _ptr(d_gate), T, E, k, _choice(SCORE, score, "score"),
-            1 if renormalize else 0, scale, _ptr(load), aux_coef, z_coef, _ptr(d_logits), on.stream(stream)))
+    _run("moe_route_backward", stream, (logits, topk_idx, d_gate, load, d_logits), _ptr(logits), _ptr(topk_idx),
+         _ptr(d_gate), T, E, k, _choice(SCORE, score, "score"), 1 if renormalize else 0, scale, _ptr(load), aux_coef,
+         z_coef, _ptr(d_logits))
     return d_logits
 
 
@@ -800,9 +792,8 @@ def moe_quantize_rows_i8(x, row_of=None, rows_max: int = 0, q=None, scale=None, 
         _rows_of(q, "q", out, cols, torch.int8)
     scale = _new((out,), torch.float32, x.device) if scale is None else \
         _rows_of(scale, "scale", out, None, torch.float32)
-    with _on(x, row_of, q, scale) as on:
-        _check("moe_quantize_rows_i8", lib().moe_quantize_rows_i8(
-            _ptr(x), _dt(x), rows, cols, _ptr(row_of), k, out, _ptr(q), _ptr(scale), on.stream(stream)))
+    _run("moe_quantize_rows_i8", stream, (x, row_of, q, scale), _ptr(x), _dt(x), rows, cols, _ptr(row_of), k, out,
+         _ptr(q), _ptr(scale))
     return q, scale
 
 
@@ -830,16 +821,14 @@ def moe_expert_gate_up_i8(x_q, x_scale, offsets, W_gu, w_scale, rows_max: int, h
     _rows_of(x_scale, "x_scale", rows, None, torch.float32)
     h = _new((rows_max, F), torch.bfloat16, x_q.device) if h is None else \
         _rows_of(h, "h", rows_max, F, torch.bfloat16)
-    with _on(x_q, x_scale, offsets, W_gu, w_scale, h, token_of_row) as on:
-        if token_of_row is None:
-            _check("moe_expert_gate_up_i8", lib().moe_expert_gate_up_i8(
-                _ptr(x_q), _ptr(x_scale), _ptr(offsets), E, d, F, rows_max, _ptr(W_gu), _ptr(w_scale), _ptr(h),
-                on.stream(stream)))
-        else:
-            _rows_of(token_of_row, "token_of_row", rows_max, None, torch.int32)
-            _check("moe_expert_gate_up_gather_i8", lib().moe_expert_gate_up_gather_i8(
-                _ptr(x_q), _ptr(x_scale), T, _ptr(token_of_row), _ptr(offsets), E, d, F, rows_max, _ptr(W_gu),
-                _ptr(w_scale), _ptr(h), on.stream(stream)))
+    if token_of_row is None:
+        _run("moe_expert_gate_up_i8", stream, (x_q, x_scale, offsets, W_gu, w_scale, h), _ptr(x_q), _ptr(x_scale),
+             _ptr(offsets), E, d, F, rows_max, _ptr(W_gu), _ptr(w_scale), _ptr(h))
+    else:
+        _rows_of(token_of_row, "token_of_row", rows_max, None, torch.int32)
+        _run("moe_expert_gate_up_gather_i8", stream, (x_q, x_scale, token_of_row, offsets, W_gu, w_scale, h),
+             _ptr(x_q), _ptr(x_scale), T, _ptr(token_of_row), _ptr(offsets), E, d, F, rows_max, _ptr(W_gu),
+             _ptr(w_scale), _ptr(h))
     return h
 
 
@@ -857,10 +846,9 @@ def moe_expert_down_i8(h_q, h_scale, offsets, W_dn, w_scale, rows_max: int, gate
         _rows_of(gate_of_row, "gate_of_row", rows_max, None, torch.float32)
     y_rows = _new((rows_max, d), y_dtype or torch.float32, h_q.device) if y_rows is None else \
         _rows_of(y_rows, "y_rows", rows_max, d, y_dtype)
-    with _on(h_q, h_scale, offsets, W_dn, w_scale, gate_of_row, y_rows) as on:
-        _check("moe_expert_down_i8", lib().moe_expert_down_i8(
-            _ptr(h_q), _ptr(h_scale), _ptr(offsets), E, d, F, rows_max, _ptr(W_dn), _ptr(w_scale), _ptr(gate_of_row),
-            _dt(y_rows), _ptr(y_rows), on.stream(stream)))
+    _run("moe_expert_down_i8", stream, (h_q, h_scale, offsets, W_dn, w_scale, gate_of_row, y_rows), _ptr(h_q),
+         _ptr(h_scale), _ptr(offsets), E, d, F, rows_max, _ptr(W_dn), _ptr(w_scale), _ptr(gate_of_row), _dt(y_rows),
+         _ptr(y_rows))
     return y_rows
 
 
@@ -901,11 +889,9 @@ def moe_block_norm(residual, y=None, post_weight=None, gate=None, alpha: float =
     G = _norm_params(d, post_weight, gate, pre_weight)
     x_out, n_out = _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, y is not None)
     rt = _dt(residual)
-    with _on(residual, y, post_weight, gate, pre_weight, x_out, n_out) as on:
-        _check("moe_block_norm", lib().moe_block_norm(
-            _ptr(residual), rt, _ptr(y), rt if y is None else _dt(y), _ptr(post_weight), _ptr(gate), G, alpha,
-            _ptr(pre_weight), eps, T, d, _ptr(x_out), _ptr(n_out), rt if n_out is None else _dt(n_out),
-            on.stream(stream)))
+    _run("moe_block_norm", stream, (residual, y, post_weight, gate, pre_weight, x_out, n_out), _ptr(residual), rt,
+         _ptr(y), rt if y is None else _dt(y), _ptr(post_weight), _ptr(gate), G, alpha, _ptr(pre_weight), eps, T, d,
+         _ptr(x_out), _ptr(n_out), rt if n_out is None else _dt(n_out))
     return x_out, n_out
 
 
@@ -928,11 +914,10 @@ def moe_combine_norm(residual, y_rows, row_of, rows_max: int, topk_gate=None, sh
     G = _norm_params(d, post_weight, gate, pre_weight)
     x_out, n_out = _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, True)
     rt = _dt(residual)
-    with _on(residual, y_rows, row_of, topk_gate, shared_y, post_weight, gate, pre_weight, y_out, x_out, n_out) as on:
-        _check("moe_combine_norm", lib().moe_combine_norm(
-            _ptr(residual), rt, _ptr(y_rows), _dt(y_rows), _ptr(row_of), _ptr(topk_gate), _ptr(shared_y), k, rows_max,
-            _ptr(post_weight), _ptr(gate), G, alpha, _ptr(pre_weight), eps, T, d, _ptr(y_out), _ptr(x_out),
-            _ptr(n_out), rt if n_out is None else _dt(n_out), on.stream(stream)))
+    _run("moe_combine_norm", stream, (residual, y_rows, row_of, topk_gate, shared_y, post_weight, gate, pre_weight, y_out, x_out, n_out),
+         _ptr(residual), rt, _ptr(y_rows), _dt(y_rows), _ptr(row_of), _ptr(topk_gate), _ptr(shared_y), k, rows_max,
+         _ptr(post_weight), _ptr(gate), G, alpha, _ptr(pre_weight), eps, T, d, _ptr(y_out), _ptr(x_out), _ptr(n_out),
+         rt if n_out is None else _dt(n_out))
     return x_out, n_out
 
 
@@ -952,10 +937,10 @@ def moe_block_norm_backward(d_x, d_n, x_out, y=None, post_weight=None, gate=None
             _need(t, n, None, (T, d))
     G = _norm_params(d, post_weight, gate, pre_weight)
 
-    def out(t, name, like, dtype):
+    def out(t, name, like, dtype):                            # in its input's shape and type
         if t is not None:
             return _need(t, name, dtype, None if like is None else like.shape)
-        return None if like is None else torch.empty_like(like, dtype=dtype)
+        return None if like is None else torch.empty_like(like)
 
     f32 = torch.float32
     d_residual = out(d_residual, "d_residual", x_out, x_out.dtype)
@@ -964,14 +949,14 @@ def moe_block_norm_backward(d_x, d_n, x_out, y=None, post_weight=None, gate=None
     d_gate = out(d_gate, "d_gate", gate, f32)
     d_pre_weight = out(d_pre_weight, "d_pre_weight", pre_weight, f32)
     rt = _dt(x_out)
-    with _on(x_out, d_x, d_n, y, post_weight, gate, pre_weight, d_residual, d_y, d_post_weight, d_gate, d_pre_weight,
-             workspace) as on:
-        nb = lib().moe_block_norm_backward_workspace_bytes(T, d)
-        ws = _ws(nb, dev, workspace)
-        _check("moe_block_norm_backward", lib().moe_block_norm_backward(
-            _ptr(d_x), _ptr(d_n), _ptr(x_out), _ptr(y), rt, rt if d_n is None else _dt(d_n), rt if y is None else _dt(y),
-            _ptr(post_weight), _ptr(gate), G, alpha, _ptr(pre_weight), eps, T, d, _ptr(d_residual), _ptr(d_y),
-            _ptr(d_post_weight), _ptr(d_gate), _ptr(d_pre_weight), _ptr(ws), nb, on.stream(stream)))
+    with torch.cuda.device(dev) if torch._C._cuda_getDevice() != x_out.get_device() else _HERE_ALREADY:
+        nb = lib().moe_block_norm_backward_workspace_bytes(T, d)     # by the current device's size
+    ws = _new((nb,), torch.uint8, dev) if workspace is None else _ws(nb, dev, workspace)
+    _run("moe_block_norm_backward", stream,
+         (x_out, d_x, d_n, y, post_weight, gate, pre_weight, d_residual, d_y, d_post_weight, d_gate, d_pre_weight, ws),
+         _ptr(d_x), _ptr(d_n), _ptr(x_out), _ptr(y), rt, rt if d_n is None else _dt(d_n), rt if y is None else _dt(y),
+         _ptr(post_weight), _ptr(gate), G, alpha, _ptr(pre_weight), eps, T, d, _ptr(d_residual), _ptr(d_y),
+         _ptr(d_post_weight), _ptr(d_gate), _ptr(d_pre_weight), _ptr(ws), nb)
     return {"d_residual": d_residual, "d_y": d_y, "d_post_weight": d_post_weight, "d_gate": d_gate,
             "d_pre_weight": d_pre_weight}
 
