@@ -21,10 +21,10 @@
 //     2 delta) is out.  What is left, about k to 2k experts, gets one lane each: its key in
 //     fp64, and its rank by counting the larger ones.  No round per selected expert.
 //   - Where the border between kept and dropped groups is closer than fp32 holds, the experts
-//     that can be among the groups' two largest are evaluated in fp64.  Where fp32 cannot decide
-//     at all (more than 32 experts left, softmax keys within 2 delta), the warp does the token
-//     again in fp64 alone.
-//   - Rows of whole 16-byte pieces come by bulk copies, one token ahead.
+//     that can be among the groups' two largest are evaluated in fp64 (softmax: and its sum, as
+//     for two candidates within 2 delta).  Where that leaves more than 32 experts, or fewer than k
+//     are unmasked, the warp does the token again in fp64 alone.
+//   - Rows of whole 16-byte pieces come by bulk copies.
 // So every selection is the fp64 one; the fp32 pass only discards what cannot be selected.
 #include <float.h>
 
@@ -244,30 +244,80 @@ struct Part {
   }
 };
 
+// Floats as integers of the same order (-0 as +0; never 0), and back.
+__device__ __forceinline__ unsigned ordered32(float v) {
+  const unsigned u = __float_as_uint(v + 0.f);
+  return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered32(unsigned o) {
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+// Doubles as integers of the same order (-0 as +0).
+__device__ __forceinline__ unsigned long long ordered(double v) {
+  const long long b = __double_as_longlong(v + 0.0);
+  return (unsigned long long)b ^ ((unsigned long long)(b >> 63) | 0x8000000000000000ull);
+}
+
+// Rank among c keys, one a lane (lanes from c on hold nothing): how many are larger, and of equal
+// ones the lower lane first.  The upper halves of the keys' integers decide, unless two lanes have
+// the same one.
+__device__ __forceinline__ int rank_of(double key, int c) {
+  const int lane = threadIdx.x & 31;
+  const unsigned long long ok = ordered(key);
+  const unsigned hi = (unsigned)(ok >> 32);
+  const unsigned same = __match_any_sync(kFull, lane < c ? hi : 0u);   // a key's half is never 0
+  int r = 0;
+  if (__all_sync(kFull, lane >= c || same == 1u << lane)) {
+    for (int j = 0; j < c; ++j) r += __shfl_sync(kFull, hi, j) > hi;
+  } else {
+    for (int j = 0; j < c; ++j) r += __shfl_sync(kFull, ok, j) > ok - (j < lane ? 1 : 0);
+  }
+  return r;
+}
+
+// Softmax: sum of exp(l - m) over a row's unmasked logits in fp64, by the warp.
+__device__ __forceinline__ double exact_sum(const float* __restrict__ l, int E, float m) {
+  double z = 0.0;
+#pragma unroll 2
+  for (int e = threadIdx.x & 31; e < E; e += 32) z += exp((double)clean_logit(__ldg(l + e)) - (double)m);
+  return wsum_d(z);
+}
+// The ranks of c candidates (expert e in this lane) by softmax + bias in fp64.
+__device__ __noinline__ int exact_softmax_order(const float* __restrict__ l, const float* __restrict__ bias, int E,
+                                                float m, int e, int c) {
+  const double z = exact_sum(l, E, m);
+  double key = -INFINITY;
+  if ((threadIdx.x & 31) < c) key = exp((double)clean_logit(__ldg(l + e)) - (double)m) / z + (double)__ldg(bias + e);
+  return rank_of(key, c);
+}
+
 // The rank of this lane's group by exact values, when the fp32 ones are too close at the border:
 // only the experts whose fp32 key is at least th (their group's second largest, or its largest,
-// less twice the error) are evaluated in fp64.  Not for softmax (its sum is not exact).
+// less twice the error) are evaluated in fp64.  m: softmax's largest logit.
 template <bool VEC, int SCORE>
 __device__ __noinline__ int exact_rank(const GroupArgs& a, const Part<VEC>& part, const float* l, const float* row,
-                                       float th) {
+                                       float th, float m) {
   const int lane = threadIdx.x & 31;
   const int L = a.team, g = lane / L;
+  const double z = SCORE == MOE_SCORE_SOFTMAX ? exact_sum(l, a.E, m) : 1.0;
   double v1 = -INFINITY, v2 = -INFINITY;
   for (int c = 0; c < part.chunks; ++c) {
     float key[4];
     part.get(row, c, key, -INFINITY);
     if (!a.bias) {                                         // the row holds logits, not scores
-      const float2 x = score32<SCORE>(clean_logit(key[0]), clean_logit(key[1]));
-      const float2 y = score32<SCORE>(clean_logit(key[2]), clean_logit(key[3]));
-      const float s[4] = {x.x, x.y, y.x, y.y};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) key[k] = key[k] > -INFINITY ? s[k] : -INFINITY;
+      for (int k = 0; k < 4; ++k) {
+        const float x = clean_logit(key[k]);
+        const float s = SCORE == MOE_SCORE_SOFTMAX ? __expf(x - m) / (float)z : score32<SCORE>(x, x).x;
+        key[k] = x > -INFINITY ? s : -INFINITY;
+      }
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (!(key[k] > -INFINITY && key[k] >= th)) continue;
       const int e = part.base + part.place(4 * c + k);
-      double v = score64((double)clean_logit(__ldg(l + e)), SCORE);
+      const double x = (double)clean_logit(__ldg(l + e));
+      double v = SCORE == MOE_SCORE_SOFTMAX ? exp(x - (double)m) / z : score64(x, SCORE);
       if (a.bias) v += (double)__ldg(a.bias + e);
       if (v > v1) { v2 = v1; v1 = v; } else if (v > v2) v2 = v;
     }
@@ -300,20 +350,6 @@ __device__ __forceinline__ float kth_of_lanes(float v, int kth) {
     }
   }
   return __shfl_sync(kFull, v, kth - 1);
-}
-
-// Floats as integers of the same order (-0 as +0; never 0), and back.
-__device__ __forceinline__ unsigned ordered32(float v) {
-  const unsigned u = __float_as_uint(v + 0.f);
-  return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float from_ordered32(unsigned o) {
-  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
-// Doubles as integers of the same order (-0 as +0).
-__device__ __forceinline__ unsigned long long ordered(double v) {
-  const long long b = __double_as_longlong(v + 0.0);
-  return (unsigned long long)b ^ ((unsigned long long)(b >> 63) | 0x8000000000000000ull);
 }
 
 // VEC: groups of whole 16-byte pieces; a warp's row comes by one bulk copy, asked for as soon as the
@@ -475,10 +511,7 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
       if (!by_logit) {                                     // the border must be wider than the error
         const float lo = from_ordered32(worst), hi = from_ordered32(__reduce_max_sync(kFull, left));
         if (!(lo - hi > 6.f * delta + 2.4e-7f * (fabsf(lo) + fabsf(hi))) && hi > -INFINITY) {
-          if (SCORE == MOE_SCORE_SOFTMAX)
-            slow = true;
-          else
-            keep = exact_rank<VEC, SCORE>(a, part, l, row, (a.top2 ? g2 : g1) - 2.f * delta) < a.kept && in_g;
+          keep = exact_rank<VEC, SCORE>(a, part, l, row, (a.top2 ? g2 : g1) - 2.f * delta, m) < a.kept && in_g;
         }
       }
     }
@@ -548,30 +581,23 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
     if (!slow) {
       double key = -INFINITY, s = 0.0;
       if (lane < c) {
-        const double lf = (double)clean_logit(biased ? __ldg(l + e) : af);
-        if (SCORE != MOE_SCORE_SOFTMAX) s = score64(lf, SCORE);
-        key = !biased ? lf : SCORE == MOE_SCORE_SOFTMAX ? (double)af : s + (double)__ldg(a.bias + e);
+        if (SCORE == MOE_SCORE_SOFTMAX && biased) {
+          key = (double)af;
+        } else {
+          key = (double)clean_logit(biased ? __ldg(l + e) : af);
+          if (SCORE != MOE_SCORE_SOFTMAX) s = score64(key, SCORE);
+          if (biased) key = s + (double)__ldg(a.bias + e);
+        }
       }
-      // rank = how many are larger; of equal ones the lower lane (index) goes first, so a lower
-      // lane counts from equal on.  The upper halves of the ordered keys decide, unless two lanes
-      // have the same one.
-      const unsigned long long ok = ordered(key);
-      const unsigned hi = (unsigned)(ok >> 32);
-      const unsigned same = __match_any_sync(kFull, lane < c ? hi : 0u);   // a key's half is never 0
-      int r = 0;
-      if (__all_sync(kFull, lane >= c || same == 1u << lane)) {
-        for (int j = 0; j < c; ++j) r += __shfl_sync(kFull, hi, j) > hi;
-      } else {
-        for (int j = 0; j < c; ++j) r += __shfl_sync(kFull, ok, j) > ok - (j < lane ? 1 : 0);
-      }
+      int r = rank_of(key, c);
       if (SCORE == MOE_SCORE_SOFTMAX && biased) {
-        // these keys are fp32: two within their error are decided in fp64
+        // these keys are fp32: where two are within their error, fp64 decides
         bool near = false;
         for (int j = 0; j < c; ++j) {
           const float o = __shfl_sync(kFull, af, j);       // by every lane, whatever it has found
           near |= fabsf(o - af) <= 2.f * delta && j != lane;
         }
-        slow = __any_sync(kFull, near && lane < c);
+        if (__any_sync(kFull, near && lane < c)) r = exact_softmax_order(l, a.bias, E, m, e, c);
       }
       if (lane < c && r < k) {                             // every lane has read its candidate
         s_cand[w][r] = e;
