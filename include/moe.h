@@ -741,8 +741,8 @@ MOE_API moe_status moe_route_grouped(const float* logits, const float* select_bi
  *   aux_coef   adds aux_coef * d aux / d logits, aux = E sum_e f_e P_e (f held constant)
  *   z_coef     adds z_coef * d z / d logits, z = mean_t lse_t^2
  *   d_logits   (device) [T, E] fp32 out (overwritten); must not overlap the inputs
- * A masked logit (-inf or NaN) has gradient 0.  An expert a token names twice takes the sum
- * of both slots' gradients.  A topk_idx entry outside [0, E) records MOE_DEVERR_EXPERT_ID
+ * A masked logit (-inf or NaN) has gradient 0, and the d_gate of its slot is not used.  An
+ * expert a token names twice takes the sum of both slots' gradients, in slot order.  A topk_idx entry outside [0, E) records MOE_DEVERR_EXPERT_ID
  * and its slot is left out.
  * Errors: INVALID_ARG for a null logits or d_logits, one of topk_idx / d_gate without the
  * other, aux_coef != 0 without load, T < 0, k < 1 or k > E with a selection, an unknown
@@ -758,9 +758,9 @@ MOE_API moe_status moe_route_backward(const float* logits, const int32_t* topk_i
  * [Handbook-Digest] "已确认", bullet "量化与推理" (routed experts kept in few bits).
  *
  * moe_quantize_rows_i8 -- q = rint(x * f) to the nearest even with f = 127 * (1 / amax) in
- *   fp32 (both steps rounded), amax the row's largest |x|, and scale = amax / 127.  A row of zeros, or with amax below
- *   2^-120, has q = 0 and scale 0; a row with an infinity or NaN has q = 0 and a NaN scale,
- *   so exactly its products are NaN.
+ *   fp32 (both steps rounded), amax the row's largest |x|, and scale = amax / 127.  A row of
+ *   zeros, or with amax below 2^-120, has q = 0 and scale 0; a row with an infinity or NaN has
+ *   q = 0 and a NaN scale, so exactly its products are NaN.
  *   Serves the activations of every step and, once at load time, the weights (a row is an
  *   output channel).
  *   x        (device) [rows, cols], x_dtype
@@ -868,8 +868,9 @@ MOE_API moe_status moe_block_norm_backward(const void* d_x, const void* d_n, con
                      float* d_gate, float* d_pre_weight, void* workspace, size_t workspace_bytes,
                      void* stream);
 
-/* Largest workspace any of the calls above needs for these sizes, for every call with
- * at most T tokens (each size query covers the batches below its T). */
+/* Largest workspace any of the forward calls above needs for these sizes, for every call with
+ * at most T tokens (each size query covers the batches below its T).
+ * moe_block_norm_backward's is moe_block_norm_backward_workspace_bytes. */
 MOE_API size_t moe_workspace_bytes(int32_t T, int32_t d, int32_t E, int32_t k);
 
 /* Reads and clears the current device's error word (synchronises `stream`).

@@ -132,7 +132,8 @@ def route_backward(logits, topk_idx, d_gate, score, renormalize, scale, load=Non
                 J = np.diag(np.where(s > 0, sig / (2.0 * s), 0.0))
         ds = np.zeros(E)                       # dL / ds
         if d_gate is not None:
-            i, u = topk_idx[t], scale * np.asarray(d_gate[t], np.float64)
+            i = topk_idx[t]
+            u = np.where(live[i], scale * np.asarray(d_gate[t], np.float64), 0.0)   # a masked slot's is not used
             if score == "softmax" and renormalize:
                 q = score_of(l[i], "softmax")
                 np.add.at(out[t], i, q * (u - q @ u))

@@ -481,10 +481,11 @@ block_norm_grad_kernel(const NormGradArgs a) {
 }
 
 // Column sums of partial rows in a fixed order: a block has 64 columns (two a lane) and 16 slices
-// of the rows, each added in fp32 (at most 30 rows), the slices in fp64.  blockIdx.y 0 and 1: the post and pre weights', over all blocks'
-// rows.  From 2 on: a gate group that two or more blocks share; its own part (slot 1) of the block
-// that begins it and the parts (slot 0) of the blocks after.  Those groups are found among the
-// groups, or among the blocks' last groups, whichever are fewer.
+// of the rows, each added in fp32 (at most 12 blocks a multiprocessor: 111 rows), the slices in
+// fp64.  blockIdx.y 0 and 1: the post and pre weights', over all blocks' rows.  From 2 on: a gate
+// group that two or more blocks share; its own part (slot 1) of the block that begins it and the
+// parts (slot 0) of the blocks after.  Those groups are found among the groups, or among the
+// blocks' last groups, whichever are fewer.
 struct ColumnArgs {
   const float* post;          // [blocks, d], or null
   const float* pre;
@@ -640,8 +641,8 @@ moe_status launch_block_norm(const void* r, int r_dtype, const void* y, int y_dt
                              const float* topk_gate, const void* shared_y, int k, long long rows_max, void* y_out,
                              const float* post, const float* gate, int G, float alpha, const float* pre, float eps,
                              int T, int d, void* x_out, void* n_out, int n_dtype, cudaStream_t s) {
-  NormArgs a{r, y, post, gate, pre, row_of, topk_gate, shared_y, y_out, x_out, n_out, rows_max, alpha, eps, 1.f / (float)d, T, d,
-             gate ? T / G : 1, k, err_ptr()};
+  NormArgs a{r, y, post, gate, pre, row_of, topk_gate, shared_y, y_out, x_out, n_out, rows_max, alpha, eps,
+             1.f / (float)d, T, d, gate ? T / G : 1, k, err_ptr()};
   if (row_of)
     return y_dtype == MOE_F32 ? norm_types<float, true>(a, r_dtype, n_dtype, s)
                               : norm_types<__nv_bfloat16, true>(a, r_dtype, n_dtype, s);

@@ -174,6 +174,7 @@ route_grad_kernel(const GradArgs a) {
       }
     }
     if (sel >= 0) lf = clean_logit(l[sel]);
+    if (!(lf > -INFINITY)) u = 0.f;                        // a masked slot gives nothing, whatever d_gate holds there
     float v[N];                                            // logits; softmax: exp(l - max) further down
     if (DENSE) {
 #pragma unroll
@@ -293,7 +294,20 @@ route_grad_kernel(const GradArgs a) {
       }
     }
     __syncwarp();
-    if (sel >= 0 && lf > -INFINITY) atomicAdd(out + sel, dk);   // a repeated expert's terms add up
+    if (gates) {
+      // a repeated expert's terms add up in slot order, in the lane of the last
+      const bool on = sel >= 0 && lf > -INFINITY;
+      const unsigned same = __match_any_sync(kFull, on ? sel : -1 - lane);
+      if (__any_sync(kFull, same != 1u << lane)) {
+        float sum = 0.f;
+        for (int j = 0; j < k; ++j) {
+          const float o = __shfl_sync(kFull, dk, j);
+          if ((same >> j) & 1u) sum += o;
+        }
+        dk = sum;
+      }
+      if (on && same >> lane == 1u) out[sel] += dk;
+    }
     if constexpr (BULK) {
       fence_proxy_async_smem();
       __syncwarp();

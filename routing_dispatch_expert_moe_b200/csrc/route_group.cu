@@ -570,6 +570,7 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
       e = s_cand[w][lane];
       af = row[e];
     }
+    if (VEC && biased) fence_proxy_async_smem();           // the keys were written before the copy writes there
     __syncwarp();                                          // the row is done with
     if (VEC && lane == 0 && t + nw < a.T) ask(l + nw * E);
     // -------------------------------------------------- exact order of what is left

@@ -249,3 +249,65 @@ def test_other_stream_and_graph_replay():
     torch.cuda.synchronize()
     assert torch.equal(i, want[0]) and torch.equal(gate, want[1]) and torch.equal(d, wantd)
     _ok()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid", "sqrt_softplus"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E", [32, 30])
+def test_a_masked_slots_upstream_gradient_is_not_used(score, renorm, E):
+    rng = np.random.default_rng(8)
+    l = rng.standard_normal((6, E)).astype(np.float32)
+    idx = np.stack([rng.permutation(E)[:4] for _ in range(6)]).astype(np.int32)
+    u = rng.standard_normal((6, 4)).astype(np.float32)
+    l[0, idx[0, 1]] = -np.inf
+    l[3, idx[3, 3]] = np.nan
+    u[0, 1] = u[3, 3] = 0.0
+    _grad(l, idx, u, score, renorm, 1.0, None, 0.0, 0.1)      # against the formula
+    M = _M()
+    on = lambda a: torch.from_numpy(a).cuda()
+    d0 = M.moe_route_backward(on(l), on(idx), on(u), score, renorm, 1.0, None, 0.0, 0.1)
+    u[0, 1], u[3, 3] = np.nan, np.inf
+    d1 = M.moe_route_backward(on(l), on(idx), on(u), score, renorm, 1.0, None, 0.0, 0.1)
+    _ok()
+    assert torch.isfinite(d0).all() and torch.equal(d0, d1)
+
+
+@pytest.mark.parametrize("E", [32, 30])
+def test_a_repeated_expert_adds_in_slot_order(E):
+    """scores without renormalising: a slot's term is s'(l) u; at l = 0 the sigmoid's s' is exactly 1/4,
+    so the sum in slot order is known to the bit: (2^24 + 1) - 2^24 rounds to 0, any order that takes
+    2^24 and -2^24 together gives 1."""
+    M = _M()
+    l = torch.zeros((5, E), device="cuda")
+    idx = torch.tensor([[3, 7, 3, 3]], dtype=torch.int32, device="cuda").repeat(5, 1)
+    u = 4.0 * torch.tensor([[2.0 ** 24, 5.0, 1.0, -2.0 ** 24]], device="cuda").repeat(5, 1)
+    d = M.moe_route_backward(l, idx, u, "sigmoid", False, 1.0)
+    _ok()
+    want = torch.zeros((5, E))
+    want[:, 7] = 5.0
+    assert torch.equal(d.cpu(), want)
+
+
+def test_refused_sizes():
+    M = _M()
+    l = torch.zeros((4, 32), device="cuda")
+    for k in (0, -1):
+        with pytest.raises(ValueError):
+            M.moe_route_grouped(l, k, 4, 2)
+    with pytest.raises(ValueError):
+        M.moe_route_backward(l, torch.empty((4, 0), dtype=torch.int32, device="cuda"), torch.empty((4, 0), device="cuda"))
+
+
+def test_many_tokens_with_a_bias_keep_their_rows():
+    """The keys replace a row in shared memory while the next row is fetched into the same place:
+    enough tokens a warp that a row is reused many times, bit-equal to one token a call."""
+    M = _M()
+    torch.manual_seed(1)
+    T, E = 9001, 64
+    l, b = torch.randn(T, E, device="cuda"), torch.randn(E, device="cuda")
+    idx, gate = M.moe_route_grouped(l, 8, 8, 4, "top2", "sigmoid", select_bias=b)
+    at = list(range(0, 128)) + list(range(T - 128, T))
+    for t in at:
+        i1, g1 = M.moe_route_grouped(l[t:t + 1], 8, 8, 4, "top2", "sigmoid", select_bias=b)
+        assert torch.equal(i1[0], idx[t]) and torch.equal(g1[0], gate[t])
+    _ok()
