@@ -186,7 +186,7 @@ class MoELayer:
         if self.routing == "learned":
             M.moe_route_grouped(self.logits[:T], self.k, self.n_groups, self.groups_kept, self.group_score, self.score,
                                 self.renormalize, self.scale, self.w.select_bias, self.topk_idx[:T],
-                                self.topk_gate[:T], stream)
+                                self.topk_gate[:T], stream=stream)
             return
         if self.routing == "noisy":
             if noise is None:
@@ -209,7 +209,8 @@ class MoELayer:
 
     def permute(self, x, stream=None):
         if self.i8:                                               # to 8 bits on the way
-            M.moe_quantize_rows_i8(x, self.row_of[:x.shape[0]], self.rows_bound, self.x_q, self.x_scale, stream)
+            M.moe_quantize_rows_i8(x, self.row_of[:x.shape[0]], self.rows_bound, self.x_q, self.x_scale,
+                                   stream=stream)
             return
         M.moe_permute(x, self.row_of[:x.shape[0]], self.rows_max, self.x_perm, stream)
 
@@ -229,7 +230,7 @@ class MoELayer:
             T = x.shape[0]
             M.moe_quantize_rows_i8(x, q=self.x_q[:T], scale=self.x_scale[:T], stream=stream)
             M.moe_expert_gate_up_i8(self.x_q[:T], self.x_scale[:T], self.offsets, *self.w.W_gu_i8, self.rows_bound,
-                                    self.h, self.token_of_row, stream)
+                                    self.h, self.token_of_row, stream=stream)
             return
         M.moe_expert_gate_up_gather(x, self.token_of_row, self.offsets, self.w.W_gu, self.rows_max, self.h, stream)
 
@@ -301,9 +302,10 @@ class MoELayer:
 
     def forward(self, x: torch.Tensor, stream=None, with_stats: bool = True, marks=None, token_id=None,
                 noise=None, combine=None) -> torch.Tensor:
-        """combine: a function (T, stream) run in place of the ordered combine (combine="rows"), whose
-        output then is the caller's own; y is not written.  marks: optional {stage name: (event, event)} recorded on the main stream right
+        """marks: optional {stage name: (event, event)} recorded on the main stream right
         before and after that stage (for timing one kernel inside the real schedule).
+        combine: a function (T, stream) run in place of the ordered combine (combine="rows"),
+        whose output then is the caller's own; y is not written.
         token_id ([T] int32, routing="hash") and noise ([T, E] f32, routing="noisy") are
         that batch's inputs of the routing rule."""
         T = x.shape[0]

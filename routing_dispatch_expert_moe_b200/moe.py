@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -681,6 +682,19 @@ def moe_router_stats(logits, counts, kept, k: int, score: str = "softmax", load=
 
 
 # ---------------------------------------------------------------- groups, 8-bit experts, block norms
+def _on_its_stream(f):
+    """With stream= another stream than the current one, the whole call runs with that stream
+    current: what it allocates, its workspace above all, is then that stream's memory, and is not
+    handed to later work of the current stream while the call's kernels still use it."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None or stream == torch.cuda.current_stream(stream.device):
+            return f(*args, stream=stream, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, stream=stream, **kw)
+    return call
+
+
 def _run(name: str, stream, tensors, *args):
     """Calls entry point `name` with args and the stream's handle, on the device that every tensor
     (None left out) is on; that device is made current for the call where it is not.  The plain
@@ -733,15 +747,18 @@ def _choice(table: dict, key: str, name: str) -> int:
     return table[key]
 
 
+@_on_its_stream
 def moe_route_grouped(logits, k: int, n_groups: int, groups_kept: int, group_score: str = "top2",
                       score: str = "sigmoid", renormalize: bool = True, scale: float = 1.0, select_bias=None,
-                      topk_idx=None, topk_gate=None, stream=None):
+                      topk_idx=None, topk_gate=None, *, stream=None):
     """Top-k of logits [T, E] within the groups_kept best of n_groups groups of neighbouring
     experts.  A -inf or NaN logit masks its expert.  Returns (topk_idx [T,k] i32, topk_gate [T,k] f32)."""
     _need(logits, "logits", torch.float32)
     T, E = logits.shape
     if select_bias is not None:
         _want(select_bias, "select_bias", torch.float32, (E,))
+    if k < 1:
+        raise ValueError(f"k must be at least 1, got {k}")
     dev = logits.device
     topk_idx = _new((T, k), torch.int32, dev) if topk_idx is None else \
         _want(topk_idx, "topk_idx", torch.int32, (T, k))
@@ -753,9 +770,10 @@ def moe_route_grouped(logits, k: int, n_groups: int, groups_kept: int, group_sco
     return topk_idx, topk_gate
 
 
+@_on_its_stream
 def moe_route_backward(logits, topk_idx=None, d_gate=None, score: str = "softmax", renormalize: bool = True,
                        scale: float = 1.0, load=None, aux_coef: float = 0.0, z_coef: float = 0.0, d_logits=None,
-                       stream=None):
+                       *, stream=None):
     """Gradient by the logits [T, E] of the gates (d_gate [T, k] of topk_idx [T, k]) plus
     aux_coef times that of the load-balancing loss (load: moe_router_stats' f_e) and z_coef times
     that of the z-loss.  Returns d_logits [T, E] f32."""
@@ -765,6 +783,8 @@ def moe_route_backward(logits, topk_idx=None, d_gate=None, score: str = "softmax
     if topk_idx is not None:
         _need(topk_idx, "topk_idx", torch.int32)
         k = topk_idx.shape[1] if topk_idx.dim() == 2 else 0
+        if k < 1:
+            raise ValueError(f"topk_idx must be [{T}, k] with k >= 1, got {tuple(topk_idx.shape)}")
         _need(topk_idx, "topk_idx", None, (T, k))
     if d_gate is not None:
         _want(d_gate, "d_gate", torch.float32, (T, k))
@@ -777,7 +797,8 @@ def moe_route_backward(logits, topk_idx=None, d_gate=None, score: str = "softmax
     return d_logits
 
 
-def moe_quantize_rows_i8(x, row_of=None, rows_max: int = 0, q=None, scale=None, stream=None):
+@_on_its_stream
+def moe_quantize_rows_i8(x, row_of=None, rows_max: int = 0, q=None, scale=None, *, stream=None):
     """Rows of x [rows, cols] (bf16 or fp32) to 8-bit integers with a scale each.  With row_of
     [rows, k] the dispatch is fused into it: token t's bytes and scale go to rows row_of[t] of q
     [rows_max, cols] (rows nothing is sent to are left as they are).  Returns (q int8, scale f32)."""
@@ -786,7 +807,9 @@ def moe_quantize_rows_i8(x, row_of=None, rows_max: int = 0, q=None, scale=None, 
     k, out = 1, rows
     if row_of is not None:
         _need(row_of, "row_of", torch.int32)
-        k, out = row_of.shape[1], rows_max
+        k, out = row_of.shape[1] if row_of.dim() == 2 else 0, rows_max
+        if k < 1:                                             # an empty row_of would pass for none
+            raise ValueError(f"row_of must be [{rows}, k] with k >= 1, got {tuple(row_of.shape)}")
         _need(row_of, "row_of", None, (rows, k))
     q = _new((out, cols), torch.int8, x.device) if q is None else \
         _rows_of(q, "q", out, cols, torch.int8)
@@ -797,7 +820,7 @@ def moe_quantize_rows_i8(x, row_of=None, rows_max: int = 0, q=None, scale=None, 
     return q, scale
 
 
-def quantize_experts_i8(W, stream=None):
+def quantize_experts_i8(W, *, stream=None):
     """Stacked expert weights W [E, N, K] (bf16 or fp32, on the device) to 8 bits with a scale for
     each output channel, once at load time.  Returns (q int8 [E, N, K], scale f32 [E, N])."""
     E, N, K = W.shape
@@ -805,14 +828,17 @@ def quantize_experts_i8(W, stream=None):
     return q.view(E, N, K), scale.view(E, N)
 
 
+@_on_its_stream
 def moe_expert_gate_up_i8(x_q, x_scale, offsets, W_gu, w_scale, rows_max: int, h=None, token_of_row=None,
-                          stream=None):
+                          *, stream=None):
     """H = silu(X Wg^T) * (X Wu^T) in bf16 from 8-bit rows x_q [rows_max, d] with x_scale [rows_max]
     and weights W_gu [E, 2F, d] int8 with w_scale [E, 2F].  With token_of_row the rows are read
     from x_q [T, d], x_scale [T] instead (moe_expert_gate_up_gather_i8)."""
     _need(W_gu, "W_gu", torch.int8)
     E, F2, d = W_gu.shape
     F = F2 // 2
+    if F2 % 2:
+        raise ValueError(f"W_gu must be [E, 2F, d], got {tuple(W_gu.shape)}")
     _want(w_scale, "w_scale", torch.float32, (E, F2))
     _want(offsets, "offsets", torch.int32, (E + 1,))
     T = x_q.shape[0]
@@ -832,8 +858,9 @@ def moe_expert_gate_up_i8(x_q, x_scale, offsets, W_gu, w_scale, rows_max: int, h
     return h
 
 
+@_on_its_stream
 def moe_expert_down_i8(h_q, h_scale, offsets, W_dn, w_scale, rows_max: int, gate_of_row=None, y_rows=None,
-                       y_dtype=None, stream=None):
+                       y_dtype=None, *, stream=None):
     """Gated rows = gate_of_row * (H W_dn^T) from 8-bit rows h_q [rows_max, F] with h_scale and
     weights W_dn [E, d, F] int8 with w_scale [E, d], in y_dtype (default: y_rows' dtype, else fp32)."""
     _need(W_dn, "W_dn", torch.int8)
@@ -852,14 +879,14 @@ def moe_expert_down_i8(h_q, h_scale, offsets, W_dn, w_scale, rows_max: int, gate
     return y_rows
 
 
-def _norm_params(d, post_weight, gate, pre_weight):
+def _norm_params(T, d, post_weight, gate, pre_weight):
     for t, n in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
         if t is not None:
             _want(t, n, torch.float32, (d,))
     if gate is None:
         return 1
     _need(gate, "gate", torch.float32)
-    if gate.dim() != 2 or gate.shape[1] != d:
+    if gate.dim() != 2 or gate.shape[1] != d or (gate.shape[0] < 1 and T > 0):
         raise ValueError(f"gate must be [rows, {d}], got {tuple(gate.shape)}")
     return gate.shape[0]
 
@@ -877,8 +904,9 @@ def _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, want_x):
     return x_out, n_out
 
 
+@_on_its_stream
 def moe_block_norm(residual, y=None, post_weight=None, gate=None, alpha: float = 1.0, pre_weight=None,
-                   eps: float = 1e-6, x_out=None, n_out=None, n_dtype=None, stream=None):
+                   eps: float = 1e-6, x_out=None, n_out=None, n_dtype=None, *, stream=None):
     """x' = alpha residual + gate * norm(y) post_weight, n = norm(x') pre_weight, on rows [T, d].
     y None: x' = alpha residual, written only if x_out is given.  gate [G, d], G dividing T.
     n_dtype defaults to n_out's, else bf16.  Returns (x_out or None, n_out or None)."""
@@ -886,7 +914,7 @@ def moe_block_norm(residual, y=None, post_weight=None, gate=None, alpha: float =
     T, d = residual.shape
     if y is not None:
         _need(y, "y", None, (T, d))
-    G = _norm_params(d, post_weight, gate, pre_weight)
+    G = _norm_params(T, d, post_weight, gate, pre_weight)
     x_out, n_out = _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, y is not None)
     rt = _dt(residual)
     _run("moe_block_norm", stream, (residual, y, post_weight, gate, pre_weight, x_out, n_out), _ptr(residual), rt,
@@ -895,9 +923,10 @@ def moe_block_norm(residual, y=None, post_weight=None, gate=None, alpha: float =
     return x_out, n_out
 
 
+@_on_its_stream
 def moe_combine_norm(residual, y_rows, row_of, rows_max: int, topk_gate=None, shared_y=None, post_weight=None,
                      gate=None, alpha: float = 1.0, pre_weight=None, eps: float = 1e-6, y_out=None, x_out=None,
-                     n_out=None, n_dtype=None, stream=None):
+                     n_out=None, n_dtype=None, *, stream=None):
     """moe_block_norm of moe_combine's sum (which y_out, if given, receives in y_rows' dtype).
     Returns (x_out, n_out or None)."""
     _need(residual, "residual")
@@ -911,19 +940,21 @@ def moe_combine_norm(residual, y_rows, row_of, rows_max: int, topk_gate=None, sh
     for t, n in ((shared_y, "shared_y"), (y_out, "y_out")):
         if t is not None:
             _want(t, n, y_rows.dtype, (T, d))
-    G = _norm_params(d, post_weight, gate, pre_weight)
+    G = _norm_params(T, d, post_weight, gate, pre_weight)
     x_out, n_out = _norm_outputs(residual, pre_weight, x_out, n_out, n_dtype, True)
     rt = _dt(residual)
-    _run("moe_combine_norm", stream, (residual, y_rows, row_of, topk_gate, shared_y, post_weight, gate, pre_weight, y_out, x_out, n_out),
+    _run("moe_combine_norm", stream,
+         (residual, y_rows, row_of, topk_gate, shared_y, post_weight, gate, pre_weight, y_out, x_out, n_out),
          _ptr(residual), rt, _ptr(y_rows), _dt(y_rows), _ptr(row_of), _ptr(topk_gate), _ptr(shared_y), k, rows_max,
          _ptr(post_weight), _ptr(gate), G, alpha, _ptr(pre_weight), eps, T, d, _ptr(y_out), _ptr(x_out), _ptr(n_out),
          rt if n_out is None else _dt(n_out))
     return x_out, n_out
 
 
+@_on_its_stream
 def moe_block_norm_backward(d_x, d_n, x_out, y=None, post_weight=None, gate=None, alpha: float = 1.0,
                             pre_weight=None, eps: float = 1e-6, d_residual=None, d_y=None, d_post_weight=None,
-                            d_gate=None, d_pre_weight=None, workspace=None, stream=None):
+                            d_gate=None, d_pre_weight=None, workspace=None, *, stream=None):
     """Gradients of moe_block_norm from its saved x_out [T, d] and y, for the gradients d_x of x_out
     and d_n of n_out (either may be None; d_n goes with pre_weight).  Returns dict(d_residual, d_y,
     d_post_weight, d_gate, d_pre_weight), None where the input is absent."""
@@ -935,7 +966,7 @@ def moe_block_norm_backward(d_x, d_n, x_out, y=None, post_weight=None, gate=None
     for t, n in ((d_n, "d_n"), (y, "y")):
         if t is not None:
             _need(t, n, None, (T, d))
-    G = _norm_params(d, post_weight, gate, pre_weight)
+    G = _norm_params(T, d, post_weight, gate, pre_weight)
 
     def out(t, name, like, dtype):                            # in its input's shape and type
         if t is not None:

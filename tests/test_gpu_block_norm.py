@@ -312,3 +312,32 @@ def test_two_graphs_and_another_stream():
     for o in outs:
         assert all(torch.equal(o[k], want[k]) for k in want)
     _ok()
+
+
+def test_an_empty_gate_is_refused():
+    M = _M()
+    x = torch.ones((4, 64), device="cuda")
+    with pytest.raises(ValueError):
+        M.moe_block_norm(x, x, gate=torch.empty((0, 64), device="cuda"))
+
+
+def test_a_given_streams_call_allocates_on_it(monkeypatch):
+    """Every call with stream= allocates its outputs and its workspace while that stream is current."""
+    M = _M()
+    st, seen = torch.cuda.Stream(), []
+    real_new, real_like = M._new, torch.empty_like
+    monkeypatch.setattr(M, "_new", lambda *a: (seen.append(torch.cuda.current_stream()), real_new(*a))[1])
+    monkeypatch.setattr(torch, "empty_like",
+                        lambda *a, **k: (seen.append(torch.cuda.current_stream()), real_like(*a, **k))[1])
+    x, w = torch.randn(8, 128, device="cuda"), torch.ones(128, device="cuda")
+    l = torch.randn(8, 32, device="cuda")
+    torch.cuda.synchronize()
+    idx, gate = M.moe_route_grouped(l, 4, 4, 2, stream=st)
+    M.moe_route_backward(l, idx, gate, stream=st)
+    q, s = M.moe_quantize_rows_i8(x, stream=st)
+    xo, n = M.moe_block_norm(x, x, post_weight=w, pre_weight=w, stream=st)
+    M.moe_block_norm_backward(x, n, xo, x, post_weight=w, pre_weight=w, stream=st)
+    assert len(seen) >= 12 and all(c == st for c in seen)
+    assert torch.cuda.current_stream() != st
+    torch.cuda.synchronize()
+    _ok()

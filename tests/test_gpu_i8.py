@@ -296,3 +296,17 @@ def test_graph_replay_and_other_stream():
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     _ok()
+
+
+def test_unsafe_or_ambiguous_arguments():
+    M = _M()
+    x = torch.ones((4, 64), device="cuda")
+    with pytest.raises(ValueError):                          # no slot: would pass for "no dispatch"
+        M.moe_quantize_rows_i8(x, torch.empty((4, 0), dtype=torch.int32, device="cuda"), 1)
+    with pytest.raises(ValueError):
+        M.moe_quantize_rows_i8(x, torch.zeros(4, dtype=torch.int32, device="cuda"), 4)
+    with pytest.raises(ValueError):                          # an odd number of weight rows
+        M.moe_expert_gate_up_i8(torch.ones((4, 128), dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda"),
+                                torch.zeros(2, dtype=torch.int32, device="cuda"),
+                                torch.ones((1, 257, 128), dtype=torch.int8, device="cuda"),
+                                torch.ones((1, 257), device="cuda"), 4)
