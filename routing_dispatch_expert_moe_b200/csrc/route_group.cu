@@ -258,9 +258,9 @@ __device__ __forceinline__ unsigned long long ordered(double v) {
   return (unsigned long long)b ^ ((unsigned long long)(b >> 63) | 0x8000000000000000ull);
 }
 
-// Rank among c keys, one a lane (lanes from c on hold nothing): how many are larger, and of equal
+// Rank among c keys, one a lane (-inf in the lanes from c on): how many are larger, and of equal
 // ones the lower lane first.  The upper halves of the keys' integers decide, unless two lanes have
-// the same one.
+// the same one.  Eight lanes' keys at a time: what lies past c outranks none of the c.
 __device__ __forceinline__ int rank_of(double key, int c) {
   const int lane = threadIdx.x & 31;
   const unsigned long long ok = ordered(key);
@@ -268,7 +268,9 @@ __device__ __forceinline__ int rank_of(double key, int c) {
   const unsigned same = __match_any_sync(kFull, lane < c ? hi : 0u);   // a key's half is never 0
   int r = 0;
   if (__all_sync(kFull, lane >= c || same == 1u << lane)) {
-    for (int j = 0; j < c; ++j) r += __shfl_sync(kFull, hi, j) > hi;
+    for (int j0 = 0; j0 < c; j0 += 8)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r += __shfl_sync(kFull, hi, j0 + j) > hi;
   } else {
     for (int j = 0; j < c; ++j) r += __shfl_sync(kFull, ok, j) > ok - (j < lane ? 1 : 0);
   }
@@ -291,17 +293,18 @@ __device__ __noinline__ int exact_softmax_order(const float* __restrict__ l, con
   return rank_of(key, c);
 }
 
-// The rank of this lane's group by exact values, when the fp32 ones are too close at the border:
-// only the experts whose fp32 key is at least th (their group's second largest, or its largest,
-// less twice the error) are evaluated in fp64.  m: softmax's largest logit.
+// The rank of this lane's group by exact values, when the fp32 ones are too close at the border.
+// sure: +1 or -1 for a group that the fp32 values put above or below every group in question, 0 for
+// those; only their experts whose fp32 key is at least th (the group's second largest, or its
+// largest, less twice the error) are evaluated in fp64.  m: softmax's largest logit.
 template <bool VEC, int SCORE>
 __device__ __noinline__ int exact_rank(const GroupArgs& a, const Part<VEC>& part, const float* l, const float* row,
-                                       float th, float m) {
+                                       float th, float m, int sure) {
   const int lane = threadIdx.x & 31;
   const int L = a.team, g = lane / L;
   const double z = SCORE == MOE_SCORE_SOFTMAX ? exact_sum(l, a.E, m) : 1.0;
   double v1 = -INFINITY, v2 = -INFINITY;
-  for (int c = 0; c < part.chunks; ++c) {
+  for (int c = 0; c < part.chunks && sure == 0; ++c) {
     float key[4];
     part.get(row, c, key, -INFINITY);
     if (!a.bias) {                                         // the row holds logits, not scores
@@ -328,7 +331,8 @@ __device__ __noinline__ int exact_rank(const GroupArgs& a, const Part<VEC>& part
     v2 = fmax(fmin(v1, c), fmax(v2, d));
     v1 = fmax(v1, c);
   }
-  const double worth = a.top2 && v2 > -INFINITY ? v1 + v2 : v1;
+  double worth = a.top2 && v2 > -INFINITY ? v1 + v2 : v1;
+  if (sure) worth = sure > 0 ? INFINITY : -INFINITY;
   int rank = 0;
   for (int o = 0; o < a.G; ++o) {
     const double c = __shfl_sync(kFull, worth, o * L);
@@ -356,7 +360,7 @@ __device__ __forceinline__ float kth_of_lanes(float v, int kth) {
 // token before has its candidates.  The row stays in shared memory, where the keys replace the
 // logits (a bias given), so that the kernel needs few registers, whatever n, and 32 warps hide its
 // chains of shuffles and fp64.  32768 tokens, 896 experts in 16 groups, k = 16: 63 us by logit,
-// 110 us for the two best of sqrt(softplus) + bias, where the 18 us of HBM time stand against some
+// 104 us for the two best of sqrt(softplus) + bias, where the 18 us of HBM time stand against some
 // 2400 instructions a token; 71 us with all groups kept (keys in registers, 24 warps: 75, 106, 124).
 template <bool VEC, int SCORE>
 __global__ void __launch_bounds__(32 * kGroupWarps, 4)
@@ -510,8 +514,11 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
       }
       if (!by_logit) {                                     // the border must be wider than the error
         const float lo = from_ordered32(worst), hi = from_ordered32(__reduce_max_sync(kFull, left));
-        if (!(lo - hi > 6.f * delta + 2.4e-7f * (fabsf(lo) + fabsf(hi))) && hi > -INFINITY) {
-          keep = exact_rank<VEC, SCORE>(a, part, l, row, (a.top2 ? g2 : g1) - 2.f * delta, m) < a.kept && in_g;
+        const float wide = 6.f * delta + 2.4e-7f * (fabsf(lo) + fabsf(hi));   // more than two values' errors
+        if (!(lo - hi > wide) && hi > -INFINITY) {
+          // above every dropped value by more than that: kept for certain; below every kept one: dropped
+          const int sure = gv - hi > wide ? 1 : lo - gv > wide ? -1 : 0;
+          keep = exact_rank<VEC, SCORE>(a, part, l, row, (a.top2 ? g2 : g1) - 2.f * delta, m, sure) < a.kept && in_g;
         }
       }
     }
