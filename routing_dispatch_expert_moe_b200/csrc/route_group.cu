@@ -24,7 +24,8 @@
 //     that can be among the groups' two largest are evaluated in fp64 (softmax: and its sum, as
 //     for two candidates within 2 delta).  Where that leaves more than 32 experts, or fewer than k
 //     are unmasked, the warp does the token again in fp64 alone.
-//   - Rows of whole 16-byte pieces come by bulk copies.
+//   - Rows of whole 16-byte pieces come by bulk copies.  A row with an infinite logit takes the
+//     fp64 path, so the scores need no clamp.
 // So every selection is the fp64 one; the fp32 pass only discards what cannot be selected.
 #include <float.h>
 
@@ -359,9 +360,11 @@ __device__ __forceinline__ float kth_of_lanes(float v, int kth) {
 // VEC: groups of whole 16-byte pieces; a warp's row comes by one bulk copy, asked for as soon as the
 // token before has its candidates.  The row stays in shared memory, where the keys replace the
 // logits (a bias given), so that the kernel needs few registers, whatever n, and 32 warps hide its
-// chains of shuffles and fp64.  32768 tokens, 896 experts in 16 groups, k = 16: 63 us by logit,
-// 104 us for the two best of sqrt(softplus) + bias, where the 18 us of HBM time stand against some
-// 2400 instructions a token; 71 us with all groups kept (keys in registers, 24 warps: 75, 106, 124).
+// chains of shuffles and fp64.  32768 tokens, 896 experts in 16 groups, k = 16, by logit: 63 us, and
+// 71 us with all groups kept (75 and 106 with the keys in registers and 24 warps).  The two best of
+// sqrt(softplus) + bias, 4 groups kept: 98 us, at 0.7 of the issue rate (reading and the largest
+// logit 26, scores 30, groups 8, candidates 19, their fp64 order and the gates 15); its bytes alone
+// need 18.
 template <bool VEC, int SCORE>
 __global__ void __launch_bounds__(32 * kGroupWarps, 4)
 route_group_kernel(const __grid_constant__ GroupArgs a) {
@@ -374,7 +377,7 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int E = a.E, n = a.n, k = a.k, L = a.team;
   const int shift = __ffs(L) - 1;                          // lanes to groups: L is a power of two
-  const float inv_n = 1.f / (float)n;
+  const unsigned inv_n = ((1u << 20) + n - 1) / n;         // rounded up
   const int pool = a.kept * n;                             // experts of the kept groups
   float* row = gsm + (size_t)w * ((E + 3) / 4 * 4);
   volatile int* abort_flag = &s_abort;
@@ -428,6 +431,7 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
     }
     // -------------------------------------------------- fp32 keys, the groups' two largest
     float m = -INFINITY, z = 0.f, delta = 0.f;
+    bool top = false;                                      // an infinite logit
     if (need_z || !by_logit) {
 #pragma unroll 4
       for (int c = 0; c < a.chunks; ++c) {
@@ -435,7 +439,9 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
         part.get(row, c, f, -INFINITY);
         m = fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), m);   // drops NaNs
       }
-      m = fminf(wmax(m), FLT_MAX);
+      m = wmax(m);
+      top = m == INFINITY;
+      m = fminf(m, FLT_MAX);
     }
     const bool dead = need_z && !(m > -INFINITY);          // every expert masked
     if (need_z && !dead) {
@@ -448,7 +454,7 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
       }
       z = wsum(z);
     }
-    bool slow = odd;
+    bool slow = odd || (top && !by_logit);
     const float iz = need_z ? __fdividef(1.f, z) : 0.f;
     auto score_of = [&](float x, float y) {
       if (SCORE == MOE_SCORE_SOFTMAX) return make_float2(__expf(x - m) * iz, __expf(y - m) * iz);
@@ -473,7 +479,7 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
         if (biased) part.get(a.bias, c, b, 0.f);
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const float x = clean_logit(f[i]), y = clean_logit(f[i + 1]);
+          const float x = f[i], y = f[i + 1];
           const float2 s = score_of(x, y);
           const float2 key = unpack2(add2(pack2(s.x, s.y), pack2(b[i], b[i + 1])));
           f[i] = x > -INFINITY ? key.x : -INFINITY;
@@ -527,13 +533,15 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
     if (!biased) delta = 0.f;                              // experts by logit, whatever the groups go by
     __syncwarp();                                          // the keys and the groups are written
     // -------------------------------------------------- candidates
-    // expert number p of the kept groups (p / n by a product: p < 1024, half a step is far off)
+    // expert number p of the kept groups (p / n by a product: with p < 1024 and an excess of inv_n n
+    // over 2^20 below n <= 1024, the quotient's excess stays below 1 / n)
     auto expert = [&](int p) {
       if (a.kept == a.G) return p;
-      const int o = (int)(((float)p + 0.5f) * inv_n);
+      const int o = (int)((unsigned)p * inv_n >> 20);
       return s_group[w][o] * n + (p - o * n);
     };
     float best = -INFINITY;
+#pragma unroll 1
     for (int p = lane; p < pool; p += 32) best = fmaxf(best, row[expert(p)]);
     best = fminf(best, FLT_MAX);
     float tau = kth_of_lanes(best, k);
@@ -541,6 +549,7 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
     auto compact = [&]() {
       const float th = tau - 2.f * delta - (delta > 0.f ? 2.4e-7f * fabsf(tau) : 0.f);
       int c = 0;
+#pragma unroll 1
       for (int p0 = 0; p0 < pool; p0 += 32) {
         const int p = p0 + lane;
         const int e = p < pool ? expert(p) : 0;
