@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(32 * kSlices)
 column_sum_kernel(const ColumnArgs a) {
   __shared__ float s[kSlices][66];
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");        // the sums' kernel is done, its stores visible
   const float* in;
   float* out;
   long long first = 0, step = a.d;
@@ -686,8 +687,17 @@ moe_status launch_block_norm_backward(const void* d_x, const void* d_n, const vo
   const bool shared = d_gate && G < T;                     // a group of one token is never shared
   const bool by_group = G <= p.blocks;
   const ColumnArgs c{a.p_post, a.p_pre, a.p_gate, d_post, d_pre, d_gate, p.blocks, d, T, T / G, by_group};
-  column_sum_kernel<<<dim3((d + 63) / 64, 2 + (shared ? by_group ? G : p.blocks : 0)), 32 * kSlices, 0, s>>>(c);
-  return check_launch();
+  // its launch overlaps the end of the kernel before it (53.5 -> 50.4 us at 8192 x 2048)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((d + 63) / 64, 2 + (shared ? by_group ? G : p.blocks : 0));
+  cfg.blockDim = dim3(32 * kSlices);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, column_sum_kernel, c));
 }
 
 }  // namespace moe
