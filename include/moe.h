@@ -789,7 +789,8 @@ MOE_API moe_status moe_route_backward(const float* logits, const int32_t* topk_i
  * Errors: INVALID_ARG for a null pointer (gate_of_row may be), a negative size or a bad
  * y_dtype; UNSUPPORTED for E > 1024, d or F not a multiple of 16 or outside [128, 16384],
  * rows_max >= 2^31, an unaligned pointer, or a driver that encodes no tensor maps.
- * Tile orientation of both GEMMs as moe_gate_up_weight_major says.
+ * Tiles are weight-major below 192 rows an expert on average (rows_max / E; gate/up) or 144
+ * (down; always for F <= 512), token-major above; MOE_B200_EXPERT_TILES overrides it here too.
  * ---------------------------------------------------------------------------------- */
 MOE_API moe_status moe_quantize_rows_i8(const void* x, int32_t x_dtype, int64_t rows, int32_t cols,
                      const int32_t* row_of, int32_t k, int64_t rows_max, int8_t* q, float* scale,

@@ -744,11 +744,14 @@ moe_status launch_tc2(const CUtensorMap& ma, const CUtensorMap& mb, const int32_
 // against the other).
 constexpr long long kWeightMajorBelow = 1024;
 
-bool prefer_weight_major(long long rows_max, int E, bool down) {
+static bool weight_major(bool by_rule) {
   const char* v = getenv("MOE_B200_EXPERT_TILES");      // read per call: a host-side string lookup
   if (v && strcmp(v, "tokens") == 0) return false;
   if (v && strcmp(v, "weights") == 0) return true;
-  return !down && E > 0 && rows_max / E < kWeightMajorBelow;
+  return by_rule;
+}
+bool prefer_weight_major(long long rows_max, int E, bool down) {
+  return weight_major(!down && E > 0 && rows_max / E < kWeightMajorBelow);
 }
 
 moe_status launch_gate_up_tc(const void* x_rows, const int32_t* offsets, int E, int d, int F, long long rows_max,
@@ -832,12 +835,24 @@ moe_status launch_gate_up_gather_tc(const void* x, const int32_t* token_of_row, 
 // the same tiles as rows of K / 2 two-byte elements (K a multiple of 16); the accumulators are
 // exact int32 sums and the epilogue multiplies them by the row's and the column's scale.  A k-block
 // holds twice the products of a bf16 one, so the epilogue has half the time: CTA pairs with eight
-// epilogue warps here, and weight-major tiles below 1024 rows an expert, for the down GEMM too.
-// Gate/up of 64 experts, 65,536 rows, d = 2048, F = 1024: 211 us (5.5e11 operations, 0.78 of twice
+// epilogue warps here, and weight-major tiles for small groups, for the down GEMM too.  Gate/up of 64 experts, 65,536 rows, d = 2048, F = 1024: 211 us (5.5e11 operations, 0.78 of twice
 // the bf16 burst rate), the tensor pipe busy 0.77 of it. ----
+
+// Weight-major below so many rows an expert on average.  Gate/up, tokens against weights (us):
+// d = 4096, F = 2048, 64 experts: 64 rows 230 / 168, 128 234 / 214, 192 279 / 265, 256 301 / 353,
+// 512 490 / 607; d = 7168, F = 256, 224 experts: 64 186 / 175, 192 225 / 229, 512 407 / 461.
+constexpr long long kI8GateUpBelow = 192;
+// Down, F above 512: 64 rows 123 / 98, 128 128 / 119, 192 151 / 168, 512 269 / 359 (d = 4096,
+// F = 2048); 128 53 / 50, 192 61 / 66 (d = 1024, F = 768).
+constexpr long long kI8DownBelow = 144;
+// F up to 512 (four k-blocks): a tile is mostly its epilogue, which the fragments make shorter.
+// F = 256: 64 rows 257 / 129, 512 738 / 538 (d = 7168), 2048 196 / 148 (d = 2048); F = 512: 64 rows
+// 31 / 24, 512 72 / 68, 2048 211 / 213.
+constexpr int kI8DownNarrow = 512;
+
 moe_status launch_gate_up_i8(const int8_t* x_q, const float* x_scale, const int32_t* offsets, int E, int d, int F,
                              long long rows_max, const int8_t* W, const float* w_scale, void* h, cudaStream_t s) {
-  if (prefer_weight_major(rows_max, E, false))
+  if (weight_major(rows_max / E < kI8GateUpBelow))
     return launch_gate_up_wm_i8(x_q, x_scale, offsets, E, d, F, rows_max, W, w_scale, h, s);
   const int K = d / 2;
   CUtensorMap ma, mb;
@@ -850,7 +865,7 @@ moe_status launch_gate_up_i8(const int8_t* x_q, const float* x_scale, const int3
 moe_status launch_down_i8(const int8_t* h_q, const float* h_scale, const int32_t* offsets, int E, int d, int F,
                           long long rows_max, const int8_t* W, const float* w_scale, const float* gate_of_row,
                           int y_dtype, void* y_rows, cudaStream_t s) {
-  if (prefer_weight_major(rows_max, E, false))
+  if (weight_major(F <= kI8DownNarrow || rows_max / E < kI8DownBelow))
     return launch_down_wm_i8(h_q, h_scale, offsets, E, d, F, rows_max, W, w_scale, gate_of_row, y_dtype, y_rows, s);
   const int K = F / 2;
   CUtensorMap ma, mb;

@@ -123,7 +123,10 @@ class MoELayer:
         if dispatch == "auto":
             # gathered where the gate/up GEMM takes weight-major tiles (the token rows are its
             # small operand, read once either way); the permute copy otherwise
-            wm = self.dtype == torch.bfloat16 and not self.fp4 and M.moe_gate_up_weight_major(self.rows_max, E)
+            if self.i8:
+                wm = self.rows_max // E < 192                     # where moe_expert_gate_up_i8 takes them
+            else:
+                wm = self.dtype == torch.bfloat16 and not self.fp4 and M.moe_gate_up_weight_major(self.rows_max, E)
             dispatch = "gather" if wm else "permute"
         self.dispatch_mode = dispatch
         R = max(self.rows_max, 1)
@@ -137,7 +140,9 @@ class MoELayer:
         self.row_of = torch.empty((T_max, k), dtype=i32, device=dev)
         self.token_of_row = torch.empty(R, dtype=i32, device=dev)
         self.gate_of_row = torch.empty(R, dtype=f32, device=dev)
-        self.x_perm = torch.empty((R, d), dtype=self.dtype, device=dev) if dispatch == "permute" and not self.i8 else None
+        self.x_perm = None
+        if dispatch == "permute" and not self.i8:
+            self.x_perm = torch.empty((R, d), dtype=self.dtype, device=dev)
         if self.i8:
             n = R if dispatch == "permute" else T_max             # rows per expert row, or per token
             self.x_q = torch.empty((n, d), dtype=torch.int8, device=dev)

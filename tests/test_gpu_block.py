@@ -143,3 +143,24 @@ def test_launch_count():
     _, _, lay2, _, _ = _block("gather", shared=False)
     # router, grouped top-k, rank, scatter, x to 8 bits, gate/up, h to 8 bits, down, combine
     assert lay.launches_per_forward(False) == 9 and lay2.launches_per_forward(False) == 9
+
+
+@pytest.mark.parametrize("T,form", [(256, "gather"), (1024, "permute")])
+def test_auto_dispatch_of_8_bit_experts_follows_their_tiles(T, form):
+    """48 and 192 rows an expert on average."""
+    from routing_dispatch_expert_moe_b200.layer import MoELayer, MoEWeights
+    from routing_dispatch_expert_moe_b200 import moe as M
+    E, d, F, k = 16, 256, 128, 3
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    w = MoEWeights(Wg=rnd(d, E) * 0.1, W_gu=None, W_dn=None, W_gu_i8=M.quantize_experts_i8(rnd(E, 2 * F, d)),
+                   W_dn_i8=M.quantize_experts_i8(rnd(E, d, F)))
+    x = rnd(T, d).bfloat16()
+    out = {}
+    for dispatch in ("auto", form):
+        lay = MoELayer(w, k=k, T_max=T, dispatch=dispatch)
+        assert dispatch != "auto" or lay.dispatch_mode == form
+        out[dispatch] = lay.forward(x).clone()
+    torch.cuda.synchronize()
+    assert M.moe_get_device_error() == 0
+    assert torch.equal(out["auto"], out[form])
