@@ -145,9 +145,9 @@ def test_launch_count():
     assert lay.launches_per_forward(False) == 9 and lay2.launches_per_forward(False) == 9
 
 
-@pytest.mark.parametrize("T,form", [(256, "gather"), (1024, "permute")])
+@pytest.mark.parametrize("T,form", [(256, "gather"), (2048, "permute")])
 def test_auto_dispatch_of_8_bit_experts_follows_their_tiles(T, form):
-    """48 and 192 rows an expert on average."""
+    """48 and 384 rows an expert on average."""
     from routing_dispatch_expert_moe_b200.layer import MoELayer, MoEWeights
     from routing_dispatch_expert_moe_b200 import moe as M
     E, d, F, k = 16, 256, 128, 3
