@@ -26,6 +26,7 @@
 // 8 us, a token's chain of reductions.
 #include <float.h>
 
+#include "f32x2.cuh"
 #include "warp_rows.cuh"
 
 namespace moe {
@@ -47,44 +48,45 @@ __device__ __forceinline__ float wsum(float v) {
 // NaN counts as masked (-inf; fmaxf drops a NaN), +inf as the largest float.
 __device__ __forceinline__ float clean_logit(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
-// exp(x) for x <= 0 within about 3 steps: 2^(x log2 e) by the exponential unit, the rounding of
+// exp(x) for two x <= 0 within about 3 steps: 2^(x log2 e) by the exponential unit, the rounding of
 // the product and the rest of log2 e made up for to first order.  0 for -inf and below 2^-126.
-__device__ __forceinline__ float exp_neg(float x) {
+__device__ __forceinline__ f32x2 exp_neg2(float x, float y) {
   constexpr float kL = 1.44269502f, kLlo = 1.92596299e-8f, kLn2 = 0.693147182f;
-  x = fmaxf(x, -200.f);
-  const float t = x * kL;
-  const float lo = fmaf(x, kLlo, fmaf(x, kL, -t));
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
-  return fmaf(r, lo * kLn2, r);
+  const f32x2 v = pack2(fmaxf(x, -200.f), fmaxf(y, -200.f));
+  const f32x2 t = mul2(v, both(kL));
+  const f32x2 lo = fma2(v, both(kLlo), fma2(v, both(kL), mul2(t, both(-1.f))));
+  const float2 u = unpack2(t);
+  float2 r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(u.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(u.y));
+  const f32x2 e = pack2(r.x, r.y);
+  return fma2(e, mul2(lo, both(kLn2)), e);
 }
 __device__ __forceinline__ float rcp_fast(float x) {       // x in [1, 2] or a normal number: 1 step
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-struct Sig {
-  float e, r;                                              // exp(-|l|), 1 / (1 + e)
-};
-__device__ __forceinline__ Sig sig_parts(float l) {
-  Sig s;
-  s.e = exp_neg(-fabsf(l));
-  s.r = rcp_fast(1.f + s.e);
-  return s;
-}
-// Score and derivative of the two scores that act on one logit alone; both 0 at -inf.
-// sigmoid = r or e r, its derivative e r^2; sqrt(softplus)' = sigmoid / (2 sqrt(softplus)).
+// Score and derivative of the two scores that act on one logit alone, for two logits; 0 at -inf.
+// sigmoid = r or e r with e = exp(-|l|), r = 1 / (1 + e), its derivative e r^2;
+// sqrt(softplus)' = sigmoid / (2 sqrt(softplus)).
 template <int SCORE>
-__device__ __forceinline__ void score_grad(float l, float* s, float* ds) {
-  const Sig p = sig_parts(l);
+__device__ __forceinline__ void score_grad2(float x, float y, f32x2* s, f32x2* ds) {
+  const f32x2 e = exp_neg2(-fabsf(x), -fabsf(y));
+  const float2 q = unpack2(add2(e, both(1.f)));
+  const f32x2 r = pack2(rcp_fast(q.x), rcp_fast(q.y));
+  const f32x2 er = mul2(e, r);
+  const float2 a = unpack2(r), b = unpack2(er);
+  const float2 sig = make_float2(x >= 0.f ? a.x : b.x, y >= 0.f ? a.y : b.y);
   if (SCORE == MOE_SCORE_SIGMOID) {
-    *s = l >= 0.f ? p.r : p.e * p.r;
-    *ds = p.e * p.r * p.r;
+    *s = pack2(sig.x, sig.y);
+    *ds = mul2(er, r);
   } else {
-    const float sig = l >= 0.f ? p.r : p.e * p.r;
-    const float root = sqrtf(fmaxf(l, 0.f) + log1pf(p.e));
-    *s = root;
-    *ds = root > 0.f ? __fdividef(sig, 2.f * root) : 0.f;
+    const float2 l = unpack2(log1p_unit(e));
+    const float2 root = make_float2(sqrtf(fmaxf(x, 0.f) + l.x), sqrtf(fmaxf(y, 0.f) + l.y));
+    *s = pack2(root.x, root.y);
+    *ds = pack2(root.x > 0.f ? __fdividef(sig.x, 2.f * root.x) : 0.f,
+                root.y > 0.f ? __fdividef(sig.y, 2.f * root.y) : 0.f);
   }
 }
 
@@ -197,11 +199,14 @@ route_grad_kernel(const GradArgs a) {
         float zs = 0.f;
         // a masked logit's exponential is 0, and so are all its terms; softmax keeps them in v
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < N; i += 2) {
           if ((i & ~3) >= used) continue;
-          const float x = exp_neg(v[i] - m);
-          if (SM) v[i] = x;
-          zs += x;
+          const float2 x = unpack2(exp_neg2(v[i] - m, v[i + 1] - m));
+          if (SM) {
+            v[i] = x.x;
+            v[i + 1] = x.y;
+          }
+          zs += x.x + x.y;
         }
         zs = wsum(zs);
         iz = 1.f / zs;
@@ -224,7 +229,12 @@ route_grad_kernel(const GradArgs a) {
         p_dot = wsum(dk);
       } else {
         float s = 0.f, ds = 0.f;
-        if (lf > -INFINITY) score_grad<SCORE>(lf, &s, &ds);
+        if (lf > -INFINITY) {
+          f32x2 s2, ds2;
+          score_grad2<SCORE>(lf, lf, &s2, &ds2);
+          s = unpack2(s2).x;
+          ds = unpack2(ds2).x;
+        }
         if (a.renorm) {
           const float tot = wsum(s), dot = wsum(s * u);
           dk = tot > 0.f ? ds * (u - dot / tot) / tot : 0.f;
@@ -237,24 +247,30 @@ route_grad_kernel(const GradArgs a) {
     float fp = 0.f, tot = 0.f;
     float s_[SM ? 1 : N];                                  // the other scores' values
     if (aux) {
+      f32x2 fp2 = both(0.f), tot2 = both(0.f);
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
         if (i >= used) continue;
         float f[4];
         fetch(a.load, i, f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 4; c += 2) {
+          const f32x2 f2 = pack2(f[c], f[c + 1]);
           if (SM) {
-            fp = fmaf(f[c], v[i + c], fp);
+            fp2 = fma2(f2, pack2(v[i + c], v[i + c + 1]), fp2);
           } else {
-            float s, ds;
-            score_grad<SCORE>(v[i + c], &s, &ds);
-            s_[SM ? 0 : i + c] = SCORE == MOE_SCORE_SIGMOID ? s : ds;
-            fp = fmaf(f[c], s, fp);
-            tot += s;
+            f32x2 s, ds;
+            score_grad2<SCORE>(v[i + c], v[i + c + 1], &s, &ds);
+            const float2 keep = unpack2(SCORE == MOE_SCORE_SIGMOID ? s : ds);
+            s_[SM ? 0 : i + c] = keep.x;
+            s_[SM ? 0 : i + c + 1] = keep.y;
+            fp2 = fma2(f2, s, fp2);
+            tot2 = add2(tot2, s);
           }
         }
       }
+      fp = sum2(fp2);
+      tot = sum2(tot2);
       fp = wsum(fp);
       if (SM) {
         fp *= iz;
@@ -274,18 +290,24 @@ route_grad_kernel(const GradArgs a) {
       if (aux) fetch(a.load, i, f, 0.f);
       if (DENSE) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float x = v[i + c];
+        for (int c = 0; c < 4; c += 2) {
+          const f32x2 f2 = pack2(f[c], f[c + 1]);
+          f32x2 g = both(0.f);
           if (SM) {
-            o[c] = x * iz * (aux ? fmaf(a.aux, f[c], flat) : flat);
+            g = aux ? fma2(both(a.aux), f2, both(flat)) : both(flat);
+            g = mul2(mul2(pack2(v[i + c], v[i + c + 1]), both(iz)), g);
           } else {
-            if (need_p && iz > 0.f) o[c] = exp_neg(x - m) * iz * flat;
+            if (need_p && iz > 0.f)
+              g = mul2(mul2(exp_neg2(v[i + c] - m, v[i + c + 1] - m), both(iz)), both(flat));
             if (aux) {
-              const float s = s_[SM ? 0 : i + c];
-              const float ds = SCORE == MOE_SCORE_SIGMOID ? fmaf(-s, s, s) : s;
-              o[c] = fmaf(inv * ds, f[c] - fp, o[c]);
+              const f32x2 s = pack2(s_[SM ? 0 : i + c], s_[SM ? 0 : i + c + 1]);
+              const f32x2 ds = SCORE == MOE_SCORE_SIGMOID ? fma2(mul2(s, both(-1.f)), s, s) : s;
+              g = fma2(mul2(both(inv), ds), add2(f2, both(-fp)), g);
             }
           }
+          const float2 h = unpack2(g);
+          o[c] = h.x;
+          o[c + 1] = h.y;
         }
       }
       if constexpr (BULK) {

@@ -88,18 +88,6 @@ __device__ __forceinline__ float sqrt_fast(float x) {
 }
 constexpr float kLog2e = 1.44269504f;
 
-// log(1 + e) on [0, 1] as e times a degree-7 polynomial fitted here for the least largest
-// relative error (2.4e-7): it keeps the relative precision of a small e.
-__device__ __forceinline__ f32x2 log1p_unit(f32x2 e) {
-  f32x2 s = fma2(both(-0.00853919890f), e, both(0.0440895967f));
-  s = fma2(s, e, both(-0.107681662f));
-  s = fma2(s, e, both(0.177452385f));
-  s = fma2(s, e, both(-0.244954616f));
-  s = fma2(s, e, both(0.332754791f));
-  s = fma2(s, e, both(-0.499974042f));
-  s = fma2(s, e, both(0.999999821f));
-  return mul2(s, e);
-}
 // fp32 scores of two logits for discarding; 0 at -inf.  The exponent l log2(e) is rounded, so the
 // error grows with |l| (2 + 1.2 |l| steps), but for l < -1 the score itself falls faster: over a
 // row the error stays below the largest score times 2e-6 + 2.4e-7 |l of the largest score|,
