@@ -24,7 +24,8 @@
 // the other's value) and over all its rows (the pre-norm weight's), and a second kernel adds the
 // blocks' partial sums in a fixed order (results repeat bit for bit).  8192 tokens, d = 2048:
 // 44 us + the sums, 50 together, where the bytes need 31: two block-wide sums a row, half the
-// issue rate.  4096 tokens, d = 7168, fp32 residual: 103, 112 together, where the bytes need 81.
+// issue rate.  4096 tokens, d = 7168, fp32 residual: 108 together (112 with pre read through the
+// first-level cache), where the bytes need 81.
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "tc_prims.cuh"
@@ -273,7 +274,8 @@ __device__ __forceinline__ void bulk_row(uint32_t dst, const void* src, uint32_t
 // while a row is reduced; each phase reads what it needs from there, and u, h and the column sums
 // stay in registers.  A buffer is filled again once every thread is past the row after it (the
 // barrier of that row's first reduction), or, with one buffer, past the row itself.
-// gate * post of the current gate group waits in shared memory (each thread its own columns).
+// gate * post of the current gate group and pre wait in shared memory (each thread its own columns):
+// the rows leave little of the first-level cache for them.
 template <typename YT, typename RT, typename NT, int V>
 __global__ void __launch_bounds__(V == 1 ? 64 : 512, V == 1 ? 12 : 1)
 block_norm_grad_kernel(const NormGradArgs a) {
@@ -288,6 +290,7 @@ block_norm_grad_kernel(const NormGradArgs a) {
   const uint32_t o_x = a.d_x ? rb : 0, o_n = o_x + (a.pre ? rb : 0), o_y = o_n + (a.pre ? nb : 0);
   const uint32_t stage_bytes = o_y + (a.y ? yb : 0);
   uint8_t* s_w = nsm + (uint32_t)a.stages * stage_bytes;   // gate * post, fp32 [d]
+  uint8_t* s_p = s_w + (a.y ? (uint32_t)a.d * 4 : 0);      // pre, fp32 [d]
   const uint32_t bar0 = smem_u32(s_bar), buf0 = smem_u32(nsm);
   volatile int* abort_flag = &s_abort;
   if (threadIdx.x == 0) {
@@ -352,6 +355,13 @@ block_norm_grad_kernel(const NormGradArgs a) {
     }
     any_post = true;
   };
+  if (a.pre) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = threadIdx.x + v * blockDim.x;
+      if (c < n8) store_oct<float>(s_p, c * 8, param8(a.pre, c * 8));
+    }
+  }
   for (int t = t0; t < t1; ++t, buf ^= 1) {
     if (t == g_end && a.y) {
       if (g >= 0) close_group();
@@ -376,7 +386,7 @@ block_norm_grad_kernel(const NormGradArgs a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = threadIdx.x + v * blockDim.x;
-        u[v] = c < n8 ? param8(a.pre, c * 8) : oct_const(0.f);
+        u[v] = c < n8 ? row8<float>(s_p, c) : oct_const(0.f);
       }
     }
     mbar_wait(bar0 + 8 * slot, parity, abort_flag, a.err);
@@ -618,13 +628,13 @@ GradPlan grad_plan(int T, int d) {
 
 template <typename YT, typename RT, typename NT, int V>
 moe_status run_grad_v(NormGradArgs a, const GradPlan& p, int threads, cudaStream_t s) {
-  constexpr size_t kSmem = 222 * 1024;                     // a multiprocessor's, less the static part
+  constexpr size_t kSmem = 226 * 1024;                     // a multiprocessor's, less the static part
   static std::atomic<int> configured[kMaxDevices];
   const moe_status st = ensure_smem_limit(configured, block_norm_grad_kernel<YT, RT, NT, V>, kSmem);
   if (st != MOE_OK) return st;
   const size_t row = (size_t)a.d * ((a.d_x ? sizeof(RT) : 0) + (a.pre ? sizeof(RT) + sizeof(NT) : 0) +
                                     (a.y ? sizeof(YT) : 0));   // at most 128 KB: one always fits
-  const size_t w = a.y ? (size_t)a.d * sizeof(float) : 0;
+  const size_t w = (size_t)a.d * sizeof(float) * ((a.y ? 1 : 0) + (a.pre ? 1 : 0));
   const size_t room = kSmem / p.per_sm - 2048 - w;
   a.stages = (int)(room / row);
   if (a.stages > kGradStages) a.stages = kGradStages;
