@@ -164,3 +164,46 @@ def test_auto_dispatch_of_8_bit_experts_follows_their_tiles(T, form):
     torch.cuda.synchronize()
     assert M.moe_get_device_error() == 0
     assert torch.equal(out["auto"], out[form])
+
+
+FIRST_CALLS = """
+import torch
+from routing_dispatch_expert_moe_b200 import moe as M
+l, x = torch.randn(64, 896, device="cuda"), torch.randn(64, 256, device="cuda").bfloat16()
+w, off = torch.ones(256, device="cuda"), torch.tensor([0, 30, 64], dtype=torch.int32, device="cuda")
+Wq, ws = torch.ones((2, 256, 256), dtype=torch.int8, device="cuda"), torch.ones((2, 256), device="cuda")
+
+def route():
+    i, g = M.moe_route_grouped(l, 8, 8, 4)
+    return g, M.moe_route_backward(l, i, g, "sigmoid", z_coef=0.1)
+
+def i8():
+    q, s = M.moe_quantize_rows_i8(x)
+    h = M.moe_expert_gate_up_i8(q, s, off, Wq, ws, 64)
+    return h, M.moe_expert_down_i8(q[:, :128].contiguous(), s, off, Wq[:, :, :128].contiguous(), ws, 64)
+
+def norm():
+    xo, n = M.moe_block_norm(x, x, w, None, 1.0, w)
+    return n, M.moe_block_norm_backward(x, x, xo, x, w, None, 1.0, w)["d_post_weight"]
+
+for f in (route, i8, norm):
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = f()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, f())), f.__name__
+    torch.cuda.synchronize()
+    assert M.moe_get_device_error() == 0
+print("captured")
+"""
+
+
+def test_a_process_first_calls_can_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
