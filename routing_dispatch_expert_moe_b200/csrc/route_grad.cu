@@ -156,6 +156,16 @@ route_grad_kernel(const GradArgs a) {
   const long long first = (long long)blockIdx.x * warps + w;
   unsigned it = 0, loaded = 0;                             // tokens done; rows asked for
   if (BULK && lane == 0 && first < a.T) rows.load(loaded++, a.logits + first * E);
+  // a token's selection and its gates' gradients are asked for a token ahead, like its row
+  int ask_sel = -1;
+  float ask_u = 0.f;
+  auto ask = [&](long long t) {
+    if (gates && lane < k && t < a.T) {
+      ask_sel = __ldg(a.topk_idx + t * k + lane);
+      ask_u = __ldg(a.d_gate + t * k + lane);
+    }
+  };
+  ask(first);
   for (long long t = first; t < a.T; t += nw, ++it) {
     const float* l = a.logits + t * E;
     float* out = reinterpret_cast<float*>(mine);           // where the row is put together
@@ -163,14 +173,15 @@ route_grad_kernel(const GradArgs a) {
     int sel = -1;
     float lf = -INFINITY, u = 0.f;
     if (gates && lane < k) {
-      sel = __ldg(a.topk_idx + t * k + lane);
+      sel = ask_sel;
       if ((unsigned)sel >= (unsigned)E) {
         record_error(a.err, MOE_DEVERR_EXPERT_ID);
         sel = -1;
       } else {
-        u = a.scale * __ldg(a.d_gate + t * k + lane);
+        u = a.scale * ask_u;
       }
     }
+    ask(t + nw);
     if constexpr (BULK) {
       if (!rows.wait(it, abort_flag, a.err)) break;
       out = rows.row(it);
