@@ -135,6 +135,12 @@ route_grad_kernel(const GradArgs a) {
   __syncthreads();
   WarpRows rows;
   uint8_t* mine = rsm + (size_t)w * (BULK ? 2 : 1) * pitch;
+  // the loads wait in shared memory, behind the rows
+  float* s_load = reinterpret_cast<float*>(rsm + (size_t)warps * (BULK ? 2 : 1) * pitch);
+  if (TERMS != kSparse && a.aux != 0.f) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) s_load[e] = __ldg(a.load + e);
+    __syncthreads();
+  }
   if (BULK) rows.init(s_bar[w], mine, pitch, lane);
   auto at = [&](int i) { return BULK ? 4 * (lane + 32 * (i >> 2)) + (i & 3) : lane + 32 * i; };
   auto fetch = [&](const float* p, int i, float (&f)[4], float none) {
@@ -144,7 +150,7 @@ route_grad_kernel(const GradArgs a) {
       f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
     } else {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) f[c] = at(i + c) < E ? __ldg(p + at(i + c)) : none;
+      for (int c = 0; c < 4; ++c) f[c] = at(i + c) < E ? p[at(i + c)] : none;
     }
   };
   const bool gates = a.d_gate != nullptr;
@@ -265,7 +271,7 @@ route_grad_kernel(const GradArgs a) {
       for (int i = 0; i < N; i += 4) {
         if (i >= used) continue;
         float f[4];
-        fetch(a.load, i, f, 0.f);
+        fetch(s_load, i, f, 0.f);
 #pragma unroll
         for (int c = 0; c < 4; c += 2) {
           const f32x2 f2 = pack2(f[c], f[c + 1]);
@@ -300,7 +306,7 @@ route_grad_kernel(const GradArgs a) {
     for (int i = 0; i < N; i += 4) {
       if (i >= used || at(i) >= E) continue;
       float o[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
-      if (aux) fetch(a.load, i, f, 0.f);
+      if (aux) fetch(s_load, i, f, 0.f);
       if (DENSE) {
 #pragma unroll
         for (int c = 0; c < 4; c += 2) {
@@ -367,11 +373,11 @@ moe_status run_grad(const GradArgs& a, cudaStream_t s) {
   const int sms = num_sms();
   int warps = (a.T + sms - 1) / sms;
   if (warps > kGradWarps) warps = kGradWarps;
-  constexpr size_t kMost = (size_t)kGradWarps * 2 * 4096;  // two rows of 1024 a warp
+  constexpr size_t kMost = (size_t)kGradWarps * 2 * 4096 + 4096;   // two rows of 1024 a warp, and the loads
   static std::atomic<int> configured[kMaxDevices];
   const moe_status st = ensure_smem_limit(configured, route_grad_kernel<NV, BULK, SCORE, TERMS>, kMost);
   if (st != MOE_OK) return st;
-  const size_t smem = (size_t)warps * (BULK ? 2 : 1) * ((a.E + 3) / 4 * 16);
+  const size_t smem = ((size_t)warps * (BULK ? 2 : 1) + (a.aux != 0.f ? 1 : 0)) * ((a.E + 3) / 4 * 16);
   long long blocks = ((long long)a.T + warps - 1) / warps;
   const long long cap = (long long)sms * (NV <= 4 ? 4 : TERMS == kBoth ? 2 : 3);   // what a multiprocessor holds
   if (blocks > cap) blocks = cap;
@@ -411,7 +417,7 @@ moe_status launch_route_backward(const float* logits, const int32_t* topk_idx, c
                                  float z_coef, float* d_logits, cudaStream_t s) {
   GradArgs a{logits, topk_idx, d_gate, load, d_logits, T, E, k, renorm, scale,
              (float)((double)aux_coef * E / T), (float)(2.0 * (double)z_coef / T), err_ptr()};
-  const bool bulk = E % 4 == 0 && aligned16(logits) && aligned16(d_logits) && aligned16(load);
+  const bool bulk = E % 4 == 0 && aligned16(logits) && aligned16(d_logits);
   if (score == MOE_SCORE_SOFTMAX) return grad_terms<MOE_SCORE_SOFTMAX>(a, bulk, s);
   if (score == MOE_SCORE_SIGMOID) return grad_terms<MOE_SCORE_SIGMOID>(a, bulk, s);
   return grad_terms<MOE_SCORE_SQRT_SOFTPLUS>(a, bulk, s);
