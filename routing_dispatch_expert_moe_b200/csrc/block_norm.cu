@@ -263,6 +263,17 @@ __device__ __forceinline__ Oct row8(const uint8_t* base, int c) {
     return oct_f32(*reinterpret_cast<const uint4*>(base + c * 32), *reinterpret_cast<const uint4*>(base + c * 32 + 16));
   }
 }
+// Eight parameters in shared memory, the first four and the last four of each eight in two halves
+// of the buffer, so that neighbouring threads' 16 bytes are neighbours.
+__device__ __forceinline__ Oct halves8(const uint8_t* base, int d, int c) {
+  const uint8_t* p = base + c * 16;
+  return oct_f32(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + d * 2));
+}
+__device__ __forceinline__ void put_halves8(uint8_t* base, int d, int c, const Oct& o) {
+  const float2 a = unpack2(o.p[0]), b = unpack2(o.p[1]), e = unpack2(o.p[2]), f = unpack2(o.p[3]);
+  *reinterpret_cast<float4*>(base + c * 16) = make_float4(a.x, a.y, b.x, b.y);
+  *reinterpret_cast<float4*>(base + d * 2 + c * 16) = make_float4(e.x, e.y, f.x, f.y);
+}
 __device__ __forceinline__ void bulk_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
@@ -359,7 +370,7 @@ block_norm_grad_kernel(const NormGradArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = threadIdx.x + v * blockDim.x;
-      if (c < n8) store_oct<float>(s_p, c * 8, param8(a.pre, c * 8));
+      if (c < n8) put_halves8(s_p, a.d, c, param8(a.pre, c * 8));
     }
   }
   for (int t = t0; t < t1; ++t, buf ^= 1) {
@@ -376,7 +387,7 @@ block_norm_grad_kernel(const NormGradArgs a) {
         Oct q = param8(gate, c * 8);
 #pragma unroll
         for (int i = 0; i < 4; ++i) q.p[i] = mul2(q.p[i], p.p[i]);
-        store_oct<float>(s_w, c * 8, q);
+        put_halves8(s_w, a.d, c, q);
       }
     }
     const long long at = (long long)t * a.d;
@@ -386,7 +397,7 @@ block_norm_grad_kernel(const NormGradArgs a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = threadIdx.x + v * blockDim.x;
-        u[v] = c < n8 ? row8<float>(s_p, c) : oct_const(0.f);
+        u[v] = c < n8 ? halves8(s_p, a.d, c) : oct_const(0.f);
       }
     }
     mbar_wait(bar0 + 8 * slot, parity, abort_flag, a.err);
@@ -441,7 +452,7 @@ block_norm_grad_kernel(const NormGradArgs a) {
       for (int i = 0; i < 4; ++i) o.p[i] = mul2(alpha, u[v].p[i]);
       store_oct<RT>(a.d_r, at + c * 8, o);
       if (!a.y) continue;
-      const Oct y = row8<YT>(st + o_y, c), w = row8<float>(s_w, c);
+      const Oct y = row8<YT>(st + o_y, c), w = halves8(s_w, a.d, c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         h[v].p[i] = mul2(u[v].p[i], w.p[i]);
