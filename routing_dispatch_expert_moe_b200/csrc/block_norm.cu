@@ -23,9 +23,9 @@
 // the rows of a gate group (the gate's and the post-norm weight's are one sum, sum_t u yh, times
 // the other's value) and over all its rows (the pre-norm weight's), and a second kernel adds the
 // blocks' partial sums in a fixed order (results repeat bit for bit).  8192 tokens, d = 2048:
-// 44 us + the sums, 50 together, where the bytes need 31: two block-wide sums a row, half the
-// issue rate.  4096 tokens, d = 7168, fp32 residual: 108 together (112 with pre read through the
-// first-level cache), where the bytes need 81.
+// 47 us with the sums, where the bytes need 31: two block-wide sums a row, half the issue rate.
+// 4096 tokens, d = 7168, fp32 residual: 104 us (110 with pre read through the first-level cache),
+// where the bytes need 81.
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "tc_prims.cuh"

@@ -21,11 +21,11 @@
 // once (exponentials, scores) what the second pass needs, in registers.  Rows come and go through
 // two shared-memory buffers a warp by bulk copies, the next one on its way while one is worked
 // on; the selected experts' terms are added to the finished row there.  32768 tokens, 896 experts,
-// sigmoid with the load-balancing loss: 60 us where the bytes need 36 (151 with plain loads and
-// stores, 62 without pairs); the exponentials and divisions take half of the issue rate.  8192
-// tokens, 64 experts: 8 us, a token's chain of reductions.  Runs of tokens a block, its warps
-// taking the next one each as they come, were slower (64): neighbouring rows are better read at
-// the same time.
+// sigmoid with the load-balancing loss: 55 us where the bytes need 36 (151 with plain loads and
+// stores); the exponentials and divisions take half of the issue rate.  8192 tokens, 64 experts:
+// 7.5 us, a token's chain of reductions.  Runs of tokens a block, its warps taking the next one
+// each as they come, were slower (64 against 60): neighbouring rows are better read at the same
+// time.
 #include <float.h>
 
 #include "f32x2.cuh"
