@@ -21,7 +21,7 @@
 // once (exponentials, scores) what the second pass needs, in registers.  Rows come and go through
 // two shared-memory buffers a warp by bulk copies, the next one on its way while one is worked
 // on; the selected experts' terms are added to the finished row there.  32768 tokens, 896 experts,
-// sigmoid with the load-balancing loss: 55 us where the bytes need 36 (151 with plain loads and
+// sigmoid with the load-balancing loss: 52 us where the bytes need 36 (151 with plain loads and
 // stores); the exponentials and divisions take half of the issue rate.  8192 tokens, 64 experts:
 // 7.5 us, a token's chain of reductions.  Runs of tokens a block, its warps taking the next one
 // each as they come, were slower (64 against 60): neighbouring rows are better read at the same
@@ -119,8 +119,11 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 // NV: chunks of four logits a lane can hold.  BULK: rows come and go through the warp's two
 // shared-memory buffers by bulk copies (rows of whole 16-byte pieces); otherwise single loads and
 // stores, and one buffer to put the row together in.
+// Above 512 experts the dense terms take two blocks a multiprocessor, without spills: 32768 tokens,
+// 896 experts 52 us (sigmoid), 55 (softmax), 80 (sqrt(softplus)), against 55, 61, 85 with three
+// blocks and 80 registers.
 template <int NV, bool BULK, int SCORE, int TERMS>
-__global__ void __launch_bounds__(32 * kGradWarps, NV <= 4 ? 4 : TERMS == kBoth ? 2 : 3)
+__global__ void __launch_bounds__(32 * kGradWarps, NV <= 4 ? 4 : TERMS == kSparse ? 3 : 2)
 route_grad_kernel(const GradArgs a) {
   constexpr int N = 4 * NV;
   constexpr bool SM = SCORE == MOE_SCORE_SOFTMAX;
@@ -379,7 +382,7 @@ moe_status run_grad(const GradArgs& a, cudaStream_t s) {
   if (st != MOE_OK) return st;
   const size_t smem = ((size_t)warps * (BULK ? 2 : 1) + (a.aux != 0.f ? 1 : 0)) * ((a.E + 3) / 4 * 16);
   long long blocks = ((long long)a.T + warps - 1) / warps;
-  const long long cap = (long long)sms * (NV <= 4 ? 4 : TERMS == kBoth ? 2 : 3);   // what a multiprocessor holds
+  const long long cap = (long long)sms * (NV <= 4 ? 4 : TERMS == kSparse ? 3 : 2);   // what a multiprocessor holds
   if (blocks > cap) blocks = cap;
   route_grad_kernel<NV, BULK, SCORE, TERMS><<<(unsigned)blocks, 32 * warps, smem, s>>>(a);
   return check_launch();
