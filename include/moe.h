@@ -846,7 +846,7 @@ MOE_API moe_status moe_expert_down_i8(const int8_t* h_q, const float* h_scale, c
  *               its input given.  Column sums are fp32 per block of tokens, then over the blocks
  *               in a fixed order: results repeat bit for bit.
  *   workspace   (device) >= moe_block_norm_backward_workspace_bytes(T, d) bytes (of the current
- *               device); calls that overlap need one each
+ *               device; 0 for sizes that the call refuses); calls that overlap need one each
  * T = 0 clears the weight gradients.
  * Errors: as above; INVALID_ARG also when a gradient is asked for without its input, or neither
  * d_x nor d_n is given; WORKSPACE if too small.

@@ -703,7 +703,7 @@ moe_status moe_combine_norm(const void* residual, int32_t r_dtype, const void* y
 }
 
 size_t moe_block_norm_backward_workspace_bytes(int32_t T, int32_t d) {
-  if (T < 1 || d < 1) return 0;
+  if (T < 1 || d < 1 || d % 8 != 0 || d > kMaxNorm || (long long)T >= kMaxT) return 0;   // what the call refuses
   return block_norm_grad_workspace_bytes(T, d);
 }
 
