@@ -561,7 +561,8 @@ column_sum_kernel(const ColumnArgs a) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int i = i0 + kSlices * k;
-        f[k] = i < n ? __ldg(reinterpret_cast<const float2*>(in + (i ? i * step : first) + c)) : make_float2(0.f, 0.f);
+        // a coherent load: these lines were written while this kernel was already resident
+        f[k] = i < n ? __ldcg(reinterpret_cast<const float2*>(in + (i ? i * step : first) + c)) : make_float2(0.f, 0.f);
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
