@@ -267,7 +267,9 @@ route_grad_kernel(const GradArgs a) {
     }
     // -------------------------------------------------- the dense terms
     float fp = 0.f, tot = 0.f;
-    float s_[SM ? 1 : N];                                  // the other scores' values
+    // the other scores' derivatives (the sigmoid's from its score, s - s^2, would lose its digits
+    // where s nears 1: 2% at a logit of 12, all of them from 17 on)
+    float ds_[SM ? 1 : N];
     if (aux) {
       f32x2 fp2 = both(0.f), tot2 = both(0.f);
 #pragma unroll
@@ -283,9 +285,9 @@ route_grad_kernel(const GradArgs a) {
           } else {
             f32x2 s, ds;
             score_grad2<SCORE>(v[i + c], v[i + c + 1], &s, &ds);
-            const float2 keep = unpack2(SCORE == MOE_SCORE_SIGMOID ? s : ds);
-            s_[SM ? 0 : i + c] = keep.x;
-            s_[SM ? 0 : i + c + 1] = keep.y;
+            const float2 keep = unpack2(ds);
+            ds_[SM ? 0 : i + c] = keep.x;
+            ds_[SM ? 0 : i + c + 1] = keep.y;
             fp2 = fma2(f2, s, fp2);
             tot2 = add2(tot2, s);
           }
@@ -322,8 +324,7 @@ route_grad_kernel(const GradArgs a) {
             if (need_p && iz > 0.f)
               g = mul2(mul2(exp_neg2(v[i + c] - m, v[i + c + 1] - m), both(iz)), both(flat));
             if (aux) {
-              const f32x2 s = pack2(s_[SM ? 0 : i + c], s_[SM ? 0 : i + c + 1]);
-              const f32x2 ds = SCORE == MOE_SCORE_SIGMOID ? fma2(mul2(s, both(-1.f)), s, s) : s;
+              const f32x2 ds = pack2(ds_[SM ? 0 : i + c], ds_[SM ? 0 : i + c + 1]);
               g = fma2(mul2(both(inv), ds), add2(f2, both(-fp)), g);
             }
           }

@@ -61,3 +61,73 @@ def test_column_sums_of_calls_that_share_a_workspace():
     for i, v in enumerate(got):
         for key, t in v.items():
             assert torch.equal(t, want[i % 2][key]), (i, key)
+
+
+# ---------------------------------------------------------------- the routing's gradient
+def _score64(l, score):
+    """Score and derivative in 64 bits, without a difference of near numbers; 0 where masked."""
+    e = np.exp(-np.abs(l))
+    sig = np.where(l >= 0, 1.0, e) / (1.0 + e)
+    if score == "sigmoid":
+        return sig, e / (1.0 + e) ** 2
+    root = np.sqrt(np.maximum(l, 0.0) + np.log1p(e))
+    return root, sig / (2.0 * np.where(root > 0, root, 1.0))
+
+
+def _parts(l, idx, u, score, renorm, load, aux):
+    """The gradient's balance term and gate term, and the sizes of what each is made of: for every
+    expert s' / S (|x| + |mean of x|)."""
+    s, ds = _score64(l, score)
+    out, size = np.zeros_like(l), np.zeros_like(l)
+    if load is not None:
+        S, f = s.sum(1, keepdims=True), load.astype(np.float64)
+        c = aux * l.shape[1] / l.shape[0]
+        mean = (s / S * f).sum(1, keepdims=True)
+        out += c * ds / S * (f - mean)
+        size += c * ds / S * (f + mean)
+    if u is not None:
+        si, di = np.take_along_axis(s, idx, 1), np.take_along_axis(ds, idx, 1)
+        u = u.astype(np.float64)
+        if renorm:
+            S = si.sum(1, keepdims=True)
+            mean, size_m = (si / S * u).sum(1, keepdims=True), (si / S * np.abs(u)).sum(1, keepdims=True)
+            g, w = di / S * (u - mean), di / S * (np.abs(u) + size_m)
+        else:
+            g, w = di * u, di * np.abs(u)
+        for t in range(len(l)):
+            out[t, idx[t]] += g[t]
+            size[t, idx[t]] += w[t]
+    return out, size
+
+
+def _relative(l, score, renorm=True, k=6, gates=True, balance=True, seed=0, floor=0.0):
+    """Every expert's gradient within 128 * 2^-24 of the sizes of its own terms.  The score, its
+    derivative and the exponentials they share are within 16 steps, sums over a row within 32 + 5
+    roundings, each of the 12 products and sums of a term half a step: under 80.  floor: what fp32's
+    smallest normal number costs, relative to the row's largest term."""
+    M = _M()
+    T, E = l.shape
+    rng = np.random.default_rng(seed)
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]) if gates else None
+    u = rng.standard_normal((T, k)).astype(np.float32) if gates else None
+    load = (rng.random(E) * 4 / E).astype(np.float32) if balance else None
+    aux = 0.25 if balance else 0.0
+    c = lambda a, t: None if a is None else torch.from_numpy(np.ascontiguousarray(a.astype(t))).cuda()
+    got = M.moe_route_backward(c(l, np.float32), c(idx, np.int32), c(u, np.float32), score, renorm, 1.0,
+                               c(load, np.float32), aux).cpu().numpy().astype(np.float64)
+    _ok()
+    want, size = _parts(l.astype(np.float32).astype(np.float64), idx, u, score, renorm, load, aux)
+    assert np.isfinite(got).all() and (np.abs(want) > 0).any()
+    tol = 128 * U * size + floor * size.max(1, keepdims=True) + 1.2e-38
+    err = np.abs(got - want)
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("at", [0.0, 6.0, 8.0, 12.0, 16.0, 20.0, 30.0])
+@pytest.mark.parametrize("score", ["sigmoid", "sqrt_softplus"])
+@pytest.mark.parametrize("E", [64, 37, 896])
+def test_balance_gradient_of_experts_that_are_hard_on(at, score, E):
+    """Logits around `at`: the sigmoid's derivative is down to e^-at and has to keep its digits."""
+    l = at + np.random.default_rng(int(at) + E).standard_normal((5, E)) * 0.5
+    _relative(l, score, gates=False)
+    _relative(l, score, k=6)
