@@ -742,8 +742,11 @@ MOE_API moe_status moe_route_grouped(const float* logits, const float* select_bi
  *   z_coef     adds z_coef * d z / d logits, z = mean_t lse_t^2
  *   d_logits   (device) [T, E] fp32 out (overwritten); must not overlap the inputs
  * A masked logit (-inf or NaN) has gradient 0, and the d_gate of its slot is not used.  An
- * expert a token names twice takes the sum of both slots' gradients, in slot order.  A topk_idx entry outside [0, E) records MOE_DEVERR_EXPERT_ID
- * and its slot is left out.
+ * expert a token names twice takes the sum of both slots' gradients, in slot order.  A topk_idx
+ * entry outside [0, E) records MOE_DEVERR_EXPERT_ID and its slot is left out.
+ * Gradients are taken in fp32; what is divided by a sum of scores keeps its relative precision where
+ * the scores are too small for fp32.  Scores below e^-745 (fp64's least) count as 0, as in
+ * moe_route_grouped; a sigmoid that is not divided counts as 0 below 2^-126.
  * Errors: INVALID_ARG for a null logits or d_logits, one of topk_idx / d_gate without the
  * other, aux_coef != 0 without load, T < 0, k < 1 or k > E with a selection, an unknown
  * score, renormalize not 0/1 or a non-finite scale or coefficient; UNSUPPORTED for E > 1024

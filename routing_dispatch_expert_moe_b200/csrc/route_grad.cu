@@ -70,25 +70,72 @@ __device__ __forceinline__ float rcp_fast(float x) {       // x in [1, 2] or a n
   return r;
 }
 // Score and derivative of the two scores that act on one logit alone, for two logits; 0 at -inf.
-// sigmoid = r or e r with e = exp(-|l|), r = 1 / (1 + e), its derivative e r^2;
-// sqrt(softplus)' = sigmoid / (2 sqrt(softplus)).
+// sigmoid = r or e r with e = exp(-|l|), r = 1 / (1 + e), its derivative e r^2.
+// sqrt(softplus) is sqrt(x) for l >= 0 and exp(l / 2) sqrt(x) below, x = l + log(1 + e) or
+// log(1 + e) / e: the factor is a number of fp32 where e itself underflows (l < -87), down to
+// l = -174.  Its derivative sigmoid / (2 sqrt(softplus)) is r / (2 sqrt(x)), times the same factor.
 template <int SCORE>
 __device__ __forceinline__ void score_grad2(float x, float y, f32x2* s, f32x2* ds) {
-  const f32x2 e = exp_neg2(-fabsf(x), -fabsf(y));
-  const float2 q = unpack2(add2(e, both(1.f)));
-  const f32x2 r = pack2(rcp_fast(q.x), rcp_fast(q.y));
-  const f32x2 er = mul2(e, r);
-  const float2 a = unpack2(r), b = unpack2(er);
-  const float2 sig = make_float2(x >= 0.f ? a.x : b.x, y >= 0.f ? a.y : b.y);
   if (SCORE == MOE_SCORE_SIGMOID) {
-    *s = pack2(sig.x, sig.y);
+    const f32x2 e = exp_neg2(-fabsf(x), -fabsf(y));
+    const float2 q = unpack2(add2(e, both(1.f)));
+    const f32x2 r = pack2(rcp_fast(q.x), rcp_fast(q.y));
+    const f32x2 er = mul2(e, r);
+    const float2 a = unpack2(r), b = unpack2(er);
+    *s = pack2(x >= 0.f ? a.x : b.x, y >= 0.f ? a.y : b.y);
     *ds = mul2(er, r);
   } else {
-    const float2 l = unpack2(log1p_unit(e));
-    const float2 root = make_float2(sqrtf(fmaxf(x, 0.f) + l.x), sqrtf(fmaxf(y, 0.f) + l.y));
-    *s = pack2(root.x, root.y);
-    *ds = pack2(root.x > 0.f ? __fdividef(sig.x, 2.f * root.x) : 0.f,
-                root.y > 0.f ? __fdividef(sig.y, 2.f * root.y) : 0.f);
+    const f32x2 half = exp_neg2(-0.5f * fabsf(x), -0.5f * fabsf(y));
+    const f32x2 e = mul2(half, half);
+    const float2 q = unpack2(add2(e, both(1.f))), h = unpack2(half);
+    const float2 p = unpack2(log1p_over(e)), l = unpack2(fma2(log1p_over(e), e, pack2(x, y)));
+    const float2 in = make_float2(x >= 0.f ? l.x : p.x, y >= 0.f ? l.y : p.y);   // at least log 2
+    const f32x2 root = pack2(rsqrtf(in.x), rsqrtf(in.y));
+    const f32x2 f = mul2(pack2(x >= 0.f ? 1.f : h.x, y >= 0.f ? 1.f : h.y), root);
+    *s = mul2(f, pack2(in.x, in.y));
+    *ds = mul2(mul2(f, pack2(rcp_fast(q.x), rcp_fast(q.y))), both(0.5f));
+  }
+}
+// Where every logit is under kDeepLogit the scores are exp(h l), h = 1 (sigmoid) or 1/2
+// (sqrt(softplus)), to fp32's precision, and may all be too small for fp32.  What is divided by their
+// sum then takes exp(h (l - m)) in their place, m the largest logit; kDeep, e^-40, is that bound for
+// the sum.  Under -745 fp64 holds no such score either, and the routing's gates are 0: so is the
+// gradient.
+constexpr float kDeep = 4e-18f, kDeepest = -745.f;
+template <int SCORE>
+constexpr float kDeepRate = SCORE == MOE_SCORE_SIGMOID ? 1.f : 0.5f;
+template <int SCORE>
+constexpr float kDeepLogit = SCORE == MOE_SCORE_SIGMOID ? -40.f : -80.f;
+
+// The dense terms of a row whose scores' sum is below kDeep, by the warp: the balance term by the
+// scores relative to the largest one, and zc = 2 z / T lse / sum exp(l - m) times exp(l - m).  One expert
+// at a time, not in the other rows' registers: such rows are rare, and their code among the others' cost
+// those 4% (896 experts, sigmoid: 54.7 us against 52.2).
+template <int SCORE>
+__device__ __forceinline__ void deep_row(const float* l, float* out, const float* load, int E, float aux, float m,
+                                      float zc) {
+  constexpr float h = kDeepRate<SCORE>;
+  const int lane = threadIdx.x & 31;
+  float top = -INFINITY, tot = 0.f, fp = 0.f;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) top = fmaxf(top, clean_logit(l[e]));
+  top = wmax(top);
+  const bool some = top >= kDeepest;
+  auto score = [&](float x) { return some ? unpack2(exp_neg2(h * (clean_logit(x) - top), 0.f)).x : 0.f; };
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) {
+    const float s = score(l[e]);
+    tot += s;
+    fp = fmaf(load[e], s, fp);
+  }
+  tot = wsum(tot);
+  fp = wsum(fp);
+  const float inv = some ? aux * h / tot : 0.f, mean = some ? fp / tot : 0.f;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) {                     // out may be l: each lane its own places
+    const float x = clean_logit(l[e]);
+    const float p = zc != 0.f ? zc * unpack2(exp_neg2(x - m, 0.f)).x : 0.f;
+    out[e] = fmaf(inv * score(x), load[e] - mean, p);
   }
 }
 
@@ -120,8 +167,8 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 // shared-memory buffers by bulk copies (rows of whole 16-byte pieces); otherwise single loads and
 // stores, and one buffer to put the row together in.
 // Above 512 experts the dense terms take two blocks a multiprocessor, without spills: 32768 tokens,
-// 896 experts 52 us (sigmoid), 55 (softmax), 80 (sqrt(softplus)), against 55, 61, 85 with three
-// blocks and 80 registers.
+// 896 experts 52 us (sigmoid) and 55 (softmax), against 55 and 61 with three blocks and 80 registers;
+// sqrt(softplus) 66 (80 with a square root and a division in place of one reciprocal root).
 template <int NV, bool BULK, int SCORE, int TERMS>
 __global__ void __launch_bounds__(32 * kGradWarps, NV <= 4 ? 4 : TERMS == kSparse ? 3 : 2)
 route_grad_kernel(const GradArgs a) {
@@ -258,6 +305,13 @@ route_grad_kernel(const GradArgs a) {
           ds = unpack2(ds2).x;
         }
         if (a.renorm) {
+          if (!__any_sync(kFull, lf > kDeepLogit<SCORE>)) {    // by every lane or none
+            const float top = wmax(lf);
+            if (top >= kDeepest) {
+              s = unpack2(exp_neg2(kDeepRate<SCORE> * (lf - top), 0.f)).x;
+              ds = kDeepRate<SCORE> * s;
+            }
+          }
           const float tot = wsum(s), dot = wsum(s * u);
           dk = tot > 0.f ? ds * (u - dot / tot) / tot : 0.f;
         } else {
@@ -307,38 +361,43 @@ route_grad_kernel(const GradArgs a) {
     // softmax: dl = p (zc - p_dot + aux (f - fp)); the constant parts together
     const float flat = a.z * lse - p_dot - (SM && aux ? a.aux * fp : 0.f);
     __syncwarp();                                          // every lane has read the row
+    const bool deep = !SM && aux && tot < kDeep;           // by every lane or none
+    if (deep) {
+      if constexpr (!SM) deep_row<SCORE>(l, out, s_load, E, a.aux, m, need_p ? iz * flat : 0.f);
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      if (i >= used || at(i) >= E) continue;
-      float o[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
-      if (aux) fetch(s_load, i, f, 0.f);
-      if (DENSE) {
+      for (int i = 0; i < N; i += 4) {
+        if (i >= used || at(i) >= E) continue;
+        float o[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
+        if (aux) fetch(s_load, i, f, 0.f);
+        if (DENSE) {
 #pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-          const f32x2 f2 = pack2(f[c], f[c + 1]);
-          f32x2 g = both(0.f);
-          if (SM) {
-            g = aux ? fma2(both(a.aux), f2, both(flat)) : both(flat);
-            g = mul2(mul2(pack2(v[i + c], v[i + c + 1]), both(iz)), g);
-          } else {
-            if (need_p && iz > 0.f)
-              g = mul2(mul2(exp_neg2(v[i + c] - m, v[i + c + 1] - m), both(iz)), both(flat));
-            if (aux) {
-              const f32x2 ds = pack2(ds_[SM ? 0 : i + c], ds_[SM ? 0 : i + c + 1]);
-              g = fma2(mul2(both(inv), ds), add2(f2, both(-fp)), g);
+          for (int c = 0; c < 4; c += 2) {
+            const f32x2 f2 = pack2(f[c], f[c + 1]);
+            f32x2 g = both(0.f);
+            if (SM) {
+              g = aux ? fma2(both(a.aux), f2, both(flat)) : both(flat);
+              g = mul2(mul2(pack2(v[i + c], v[i + c + 1]), both(iz)), g);
+            } else {
+              if (need_p && iz > 0.f)
+                g = mul2(mul2(exp_neg2(v[i + c] - m, v[i + c + 1] - m), both(iz)), both(flat));
+              if (aux) {
+                const f32x2 ds = pack2(ds_[SM ? 0 : i + c], ds_[SM ? 0 : i + c + 1]);
+                g = fma2(mul2(both(inv), ds), add2(f2, both(-fp)), g);
+              }
             }
+            const float2 h = unpack2(g);
+            o[c] = h.x;
+            o[c + 1] = h.y;
           }
-          const float2 h = unpack2(g);
-          o[c] = h.x;
-          o[c + 1] = h.y;
         }
-      }
-      if constexpr (BULK) {
-        *reinterpret_cast<float4*>(out + at(i)) = make_float4(o[0], o[1], o[2], o[3]);
-      } else {
+        if constexpr (BULK) {
+          *reinterpret_cast<float4*>(out + at(i)) = make_float4(o[0], o[1], o[2], o[3]);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (at(i + c) < E) out[at(i + c)] = o[c];
+          for (int c = 0; c < 4; ++c)
+            if (at(i + c) < E) out[at(i + c)] = o[c];
+        }
       }
     }
     __syncwarp();

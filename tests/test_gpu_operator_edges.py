@@ -117,7 +117,7 @@ def _relative(l, score, renorm=True, k=6, gates=True, balance=True, seed=0, floo
                                c(load, np.float32), aux).cpu().numpy().astype(np.float64)
     _ok()
     want, size = _parts(l.astype(np.float32).astype(np.float64), idx, u, score, renorm, load, aux)
-    assert np.isfinite(got).all() and (np.abs(want) > 0).any()
+    assert np.isfinite(got).all() and (k == 1 or (np.abs(want) > 0).any())   # one gate alone is always 1
     tol = 128 * U * size + floor * size.max(1, keepdims=True) + 1.2e-38
     err = np.abs(got - want)
     assert (err <= tol).all(), float((err / tol).max())
@@ -131,3 +131,73 @@ def test_balance_gradient_of_experts_that_are_hard_on(at, score, E):
     l = at + np.random.default_rng(int(at) + E).standard_normal((5, E)) * 0.5
     _relative(l, score, gates=False)
     _relative(l, score, k=6)
+
+
+@pytest.mark.parametrize("at", [-30.0, -60.0, -88.0, -100.0, -150.0, -300.0, -700.0])
+@pytest.mark.parametrize("score", ["sigmoid", "sqrt_softplus"])
+@pytest.mark.parametrize("E,k", [(64, 6), (37, 5), (896, 16), (12, 1)])
+def test_gradient_of_scores_that_fp32_cannot_hold(at, score, E, k):
+    """Rows far below 0, whose scores' ratios are ordinary numbers: the routing gives them ordinary
+    gates, and the gradient follows.  A score below e^-87 of the largest counts as 0."""
+    l = at + np.random.default_rng(int(-at) + E).standard_normal((7, E)) * 1.5
+    _relative(l, score, True, k, gates=False, floor=1e-30)
+    _relative(l, score, True, k, balance=False, floor=1e-30)
+    _relative(l, score, True, k, floor=1e-30)
+
+
+@pytest.mark.parametrize("E", [64, 61])
+def test_gradient_of_sqrt_softplus_below_zero(E):
+    """Not divided by a sum, and next to larger ones: exp(l / 2) is a number of fp32 down to -174."""
+    rng = np.random.default_rng(E)
+    l = rng.uniform(-170.0, 10.0, (9, E))
+    _relative(l, "sqrt_softplus", False, balance=False)
+    _relative(l, "sqrt_softplus", True)
+    _relative(rng.uniform(-170.0, -90.0, (9, E)), "sqrt_softplus", False, balance=False)
+    _relative(rng.uniform(-80.0, 10.0, (9, E)), "sigmoid", False, balance=False)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "sqrt_softplus"])
+@pytest.mark.parametrize("shift", [0.0, -100.0, -150.0])
+def test_masked_experts_and_rows_with_a_balance_term(score, shift):
+    rng = np.random.default_rng(9)
+    l = shift + rng.standard_normal((6, 32))
+    l[0, ::3] = -np.inf
+    l[1, 1:] = -np.inf                                       # one expert left
+    l[2] = -np.inf                                           # none
+    l[3] = -800.0                                            # no score is a number of fp64: gates 0
+    _relative_masked(l, score)
+
+
+def _relative_masked(l, score):
+    M = _M()
+    rng = np.random.default_rng(1)
+    T, E = l.shape
+    idx = np.stack([rng.permutation(E)[:4] for _ in range(T)])
+    u = rng.standard_normal((T, 4)).astype(np.float32)
+    load = (rng.random(E) * 4 / E).astype(np.float32)
+    c = lambda a, t: torch.from_numpy(np.ascontiguousarray(a.astype(t))).cuda()
+    got = M.moe_route_backward(c(l, np.float32), c(idx, np.int32), c(u, np.float32), score, True, 1.0,
+                               c(load, np.float32), 0.25).cpu().numpy().astype(np.float64)
+    _ok()
+    l32 = l.astype(np.float32).astype(np.float64)
+    dead = ~(l32 > -745.0).any(1)
+    live = l32 > -np.inf
+    u = np.where(np.take_along_axis(live, idx, 1), u, 0.0)
+    for t in range(T):
+        if dead[t]:
+            assert (got[t] == 0).all()
+            continue
+        want, size = np.zeros((1, E)), np.zeros((1, E))
+        s, ds = _score64(l32[t], score)
+        S, c_ = s.sum(), 0.25 * E / T
+        mean = (s * load).sum() / S
+        want[0] += c_ * ds / S * (load - mean)
+        size[0] += c_ * ds / S * (load + mean)
+        si = s[idx[t]]
+        if si.sum() > 0:
+            mu, ma = (si * u[t]).sum() / si.sum(), (si * np.abs(u[t])).sum() / si.sum()
+            want[0, idx[t]] += ds[idx[t]] / si.sum() * (u[t] - mu)
+            size[0, idx[t]] += ds[idx[t]] / si.sum() * (np.abs(u[t]) + ma)
+        want[0, ~live[t]] = 0.0
+        tol = 128 * U * size[0] + 1e-30 * size.max() + 1.2e-38
+        assert (np.abs(got[t] - want[0]) <= tol).all() and (got[t][~live[t]] == 0).all()
