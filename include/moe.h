@@ -713,7 +713,9 @@ MOE_API moe_status moe_expert_down_fp4(const void* h, const int32_t* offsets, in
  * lower index, the order is key descending, then index ascending.
  *   logits       (device) [T, E] fp32 (moe_router_logits)
  *   select_bias  (device) [E] fp32 or NULL
- *   score, renormalize, scale: as moe_route (the gates are taken in fp64 and rounded once)
+ *   score, renormalize, scale: as moe_route.  The gates are taken in fp64 and rounded once, but for
+ *                softmax without renormalize: its denominator, over all E experts, is a sum in fp32
+ *                (within 120 * 2^-24 of the exact one)
  *   topk_idx     (device) [T, k] int32 out;  topk_gate (device) [T, k] fp32 out
  * A logit of -inf or NaN masks its expert: its key is -inf whatever its bias, it adds
  * nothing to its group, and its gate is 0 where it is selected all the same (fewer than k

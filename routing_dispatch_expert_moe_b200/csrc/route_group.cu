@@ -1,9 +1,8 @@
-// Group-limited top-k routing of given logits, and the gradient of a routing.
+// Group-limited top-k routing of given logits.
 //
 // Handbook news post (hub.geekagi.cn), "真正难在三个环节" item 2 (a bias for balance that only
 // selects) and the quoted tweet (softmax, sigmoid, sqrt(softplus) scores); "Hugging Face 图解
-// Mixture of Experts（MoE）原理、训练与推理权衡", section "什么是稀疏性？" (KeepTopK, gates) and
-// the sections on the load-balancing loss and the router z-loss.
+// Mixture of Experts（MoE）原理、训练与推理权衡", section "什么是稀疏性？" (KeepTopK, gates).
 //
 // moe_route_grouped.  The E experts form G groups of n = E / G.  An expert's key is its logit,
 // or score + bias in fp64; a group's value is its largest key, or the sum of its two largest
@@ -26,7 +25,11 @@
 //     are unmasked, the warp does the token again in fp64 alone.
 //   - Rows of whole 16-byte pieces come by bulk copies.  A row with an infinite logit takes the
 //     fp64 path, so the scores need no clamp.
-// So every selection is the fp64 one; the fp32 pass only discards what cannot be selected.
+// So every selection is the fp64 one; the fp32 pass only discards what cannot be selected.  The gates
+// are fp64 too, but for the softmax's denominator over all experts (without renormalising), which
+// is the fp32 pass's sum: at most 64 + 5 additions, 2 steps an exponential and half a step of each
+// difference.  Summed in fp64 it took 121 us by a polynomial and 147 by exp() where this takes 80
+// (32768 tokens, 896 experts, groups by their largest key).
 #include <float.h>
 
 #include "common.cuh"
@@ -615,7 +618,7 @@ route_group_kernel(const __grid_constant__ GroupArgs a) {
       }
     }
     if (slow) pick = route_token_fp64<SCORE>(a, l);
-    // -------------------------------------------------- gates (fp64, rounded once)
+    // -------------------------------------------------- gates (fp64, rounded once; pick.z: see above)
     double s = 0.0;
     if (SCORE == MOE_SCORE_SOFTMAX) {
       const float lf = lane < k ? clean_logit(__ldg(l + pick.idx)) : -INFINITY;

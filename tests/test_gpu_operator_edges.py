@@ -201,3 +201,24 @@ def _relative_masked(l, score):
         want[0, ~live[t]] = 0.0
         tol = 128 * U * size[0] + 1e-30 * size.max() + 1.2e-38
         assert (np.abs(got[t] - want[0]) <= tol).all() and (got[t][~live[t]] == 0).all()
+
+
+# ---------------------------------------------------------------- the routing's gates
+@pytest.mark.parametrize("T,E,k,G,kept", [(64, 896, 16, 16, 4), (64, 1024, 8, 1, 1), (33, 255, 5, 3, 2), (64, 8, 2, 4, 2)])
+@pytest.mark.parametrize("spread", [0.0, 0.01, 1.0, 12.0])
+def test_full_softmax_gates_are_within_the_stated_bound(T, E, k, G, kept, spread):
+    """Without renormalising: the denominator over all experts is within 120 * 2^-24 (at spread 0
+    with a bias every key is equal, and a token is taken in fp64, or its terms are few and all 1)."""
+    M = _M()
+    l = (np.random.default_rng(E).standard_normal((T, E)) * spread).astype(np.float32)
+    for bias in (None, np.zeros(E, np.float32)):
+        on = None if bias is None else torch.from_numpy(bias).cuda()
+        for gs in ("max", "top2"):
+            i, g = M.moe_route_grouped(torch.from_numpy(l).cuda(), k, G, kept, gs, "softmax", False, 1.0, on)
+            _ok()
+            p = np.exp(l.astype(np.float64) - l.max(1, keepdims=True))
+            want = np.take_along_axis(p / p.sum(1, keepdims=True), i.cpu().numpy().astype(np.int64), 1)
+            err = np.abs(g.cpu().numpy() - want) / want
+            assert err.max() <= 121 * U
+            if spread == 0.0 and bias is not None:
+                assert err.max() <= U * 1.001               # rounded once
