@@ -438,10 +438,14 @@ class MoEBlock:
     layer: a MoELayer with combine="rows".  pre_weight, post_weight, next_weight: [d] f32 or None;
     gate: [G, d] f32 or None, G dividing the tokens of every call.  residual_dtype: that of the
     stream (the normed rows are bf16 or fp32 as the layer takes them).  Buffers for T_max tokens
-    are allocated here; what forward returns are views of them, valid until the next call."""
+    are allocated here; what forward returns are views of them, valid until the next call.
+    keep_y: also keep y, rounded to the layer's rows_dtype, in self.y (for the last call's tokens):
+    with x', what moe_block_norm_backward takes for the gradients behind the layer (its post_weight,
+    gate, alpha and eps are the block's, its pre_weight next_weight)."""
 
     def __init__(self, layer: MoELayer, pre_weight, post_weight=None, gate=None, alpha: float = 1.0,
-                 next_weight=None, eps: float = 1e-6, residual_dtype: torch.dtype = torch.bfloat16):
+                 next_weight=None, eps: float = 1e-6, residual_dtype: torch.dtype = torch.bfloat16,
+                 keep_y: bool = False):
         if layer.combine_mode != "rows":
             raise ValueError("a block needs a layer with combine='rows'")
         if pre_weight is None:
@@ -452,6 +456,7 @@ class MoEBlock:
         self.n = torch.empty((T, d), dtype=layer.dtype, device=dev)
         self.x_out = torch.empty((T, d), dtype=residual_dtype, device=dev)
         self.n_out = torch.empty((T, d), dtype=layer.dtype, device=dev) if next_weight is not None else None
+        self.y = torch.empty((T, d), dtype=layer.rows_dtype, device=dev) if keep_y else None
 
     def forward(self, residual: torch.Tensor, n: Optional[torch.Tensor] = None, stream=None, with_stats: bool = True):
         """residual [T, d]; n: its pre-norm, where the block before gave it (its n').  Returns
@@ -465,12 +470,13 @@ class MoEBlock:
             M.moe_block_norm(residual, pre_weight=self.pre_weight, eps=self.eps, n_out=n, stream=s)
         x_out = self.x_out[:T]
         n_out = None if self.n_out is None else self.n_out[:T]
+        y_out = None if self.y is None else self.y[:T]
 
         def combine(T_, s_):
             M.moe_combine_norm(residual, lay.y_perm, lay.row_of[:T_], lay.rows_max,
                                shared_y=lay.y_s[:T_] if lay.has_shared else None, post_weight=self.post_weight,
                                gate=self.gate, alpha=self.alpha, pre_weight=self.next_weight, eps=self.eps,
-                               x_out=x_out, n_out=n_out, stream=s_)
+                               y_out=y_out, x_out=x_out, n_out=n_out, stream=s_)
 
         lay.forward(n, stream=s, with_stats=with_stats, combine=combine)
         return x_out, n_out

@@ -207,3 +207,49 @@ def test_a_process_first_calls_can_be_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("rows", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("t", [300, 33])
+def test_a_block_keeps_what_its_norms_gradients_take(rows, t):
+    """y as the combine sums it, rounded once; the gradients behind the layer from it and x'."""
+    from routing_dispatch_expert_moe_b200.layer import MoEBlock, MoELayer
+    M, w, lay, blk, r = _block("permute")
+    lay = MoELayer(w, K, T, "sigmoid", True, 2.0, -1, rows_dtype=rows, n_groups=4, groups_kept=2)
+    args = (blk.pre_weight, blk.post_weight, blk.gate, 0.5, blk.next_weight)
+    kept = MoEBlock(lay, *args, keep_y=True)
+    x, n = (v.clone() for v in MoEBlock(lay, *args).forward(r[:t]))
+    x2, n2 = kept.forward(r[:t])
+    y = kept.y[:t]
+    torch.cuda.synchronize()
+    assert M.moe_get_device_error() == 0
+    assert torch.equal(x, x2) and torch.equal(n, n2)         # keeping y changes nothing else
+    row_of = lay.row_of[:t].cpu().numpy()
+    used = int(lay.offsets[-1])
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g) * 0.1
+    want_y = B.combine_sum(_n(lay.y_perm[:used]), row_of, None, _n(lay.y_s[:t]))
+    size = B.combine_sum(np.abs(_n(lay.y_perm[:used])), row_of, None, np.abs(_n(lay.y_s[:t])))
+    half = 2.0 ** -8 if rows == torch.bfloat16 else U
+    assert y.dtype == rows and (np.abs(_n(y) - want_y) <= (K + 1) * U * size + half * np.abs(want_y)).all()
+    dx, dn = rnd(t, D).bfloat16(), rnd(t, D).bfloat16()
+    got = M.moe_block_norm_backward(dx, dn, x2, y, blk.post_weight, blk.gate, 0.5, blk.next_weight, kept.eps)
+    torch.cuda.synchronize()
+    assert M.moe_get_device_error() == 0
+    want = B.block_norm_backward(_n(dx), _n(dn), _n(x2), _n(y), _n(blk.post_weight), _n(blk.gate), 0.5,
+                                 _n(blk.next_weight), kept.eps)
+    # the bars of the norms' own tests: (256 + T) roundings of the sums of the terms' sizes
+    rx = 1.0 / np.sqrt((_n(x2) ** 2).mean(1, keepdims=True) + kept.eps)
+    xh, gs = np.abs(_n(x2)) * rx, np.abs(_n(dn) * _n(blk.next_weight))
+    u = np.abs(_n(dx)) + rx * (gs + xh * (gs * xh).mean(1, keepdims=True))
+    yr = 1.0 / np.sqrt((_n(y) ** 2).mean(1, keepdims=True) + kept.eps)
+    yh = np.abs(_n(y)) * yr
+    sizes = {"d_residual": 0.5 * u, "d_pre_weight": (np.abs(_n(dn)) * xh).sum(0),
+             "d_gate": (u * yh * np.abs(_n(blk.post_weight))).reshape(3, -1, D).sum(1)}
+    ug = u * np.repeat(np.abs(_n(blk.gate)), t // 3, axis=0)
+    sizes["d_post_weight"] = (ug * yh).sum(0)
+    h = ug * np.abs(_n(blk.post_weight))
+    sizes["d_y"] = yr * (h + yh * (h * yh).mean(1, keepdims=True))
+    for key, sz in sizes.items():
+        step = {"d_residual": 2.0 ** -8, "d_y": half}.get(key, U)
+        assert (np.abs(_n(got[key]) - want[key]) <= (256 + t) * U * sz + step * np.abs(want[key]) + 1e-30).all(), key
