@@ -450,6 +450,8 @@ class MoEBlock:
             raise ValueError("a block needs a layer with combine='rows'")
         if pre_weight is None:
             raise ValueError("a block needs pre_weight (pass n to forward to skip the norm)")
+        if gate is not None and (gate.dim() != 2 or gate.shape[0] < 1 or gate.shape[1] != layer.d):
+            raise ValueError(f"gate must be [rows, {layer.d}], got {tuple(gate.shape)}")
         self.layer, self.pre_weight, self.post_weight, self.next_weight = layer, pre_weight, post_weight, next_weight
         self.gate, self.alpha, self.eps = gate, alpha, eps
         T, d, dev = layer.T_max, layer.d, layer.device
@@ -464,6 +466,13 @@ class MoEBlock:
         lay, T = self.layer, residual.shape[0]
         if T > lay.T_max:
             raise ValueError(f"T={T} exceeds T_max={lay.T_max}")
+        # all that the last stage would refuse, before the first one is launched
+        if residual.shape != (T, lay.d) or residual.dtype != self.x_out.dtype:
+            raise ValueError(f"residual must be [T, {lay.d}] {self.x_out.dtype}, got {tuple(residual.shape)} {residual.dtype}")
+        if n is not None and n.shape != (T, lay.d):
+            raise ValueError(f"n must have shape {(T, lay.d)}, got {tuple(n.shape)}")
+        if self.gate is not None and T % self.gate.shape[0]:
+            raise ValueError(f"the gate's {self.gate.shape[0]} rows do not divide the {T} tokens")
         s = torch.cuda.current_stream() if stream is None else stream
         if n is None:
             n = self.n[:T]
