@@ -460,9 +460,10 @@ class MoEBlock:
         self.n_out = torch.empty((T, d), dtype=layer.dtype, device=dev) if next_weight is not None else None
         self.y = torch.empty((T, d), dtype=layer.rows_dtype, device=dev) if keep_y else None
 
-    def forward(self, residual: torch.Tensor, n: Optional[torch.Tensor] = None, stream=None, with_stats: bool = True):
-        """residual [T, d]; n: its pre-norm, where the block before gave it (its n').  Returns
-        (x', n' or None)."""
+    def forward(self, residual: torch.Tensor, n: Optional[torch.Tensor] = None, stream=None, with_stats: bool = True,
+                token_id=None, noise=None):
+        """residual [T, d]; n: its pre-norm, where the block before gave it (its n'); token_id,
+        noise: the routing rule's inputs (MoELayer.forward).  Returns (x', n' or None)."""
         lay, T = self.layer, residual.shape[0]
         if T > lay.T_max:
             raise ValueError(f"T={T} exceeds T_max={lay.T_max}")
@@ -487,5 +488,5 @@ class MoEBlock:
                                gate=self.gate, alpha=self.alpha, pre_weight=self.next_weight, eps=self.eps,
                                y_out=y_out, x_out=x_out, n_out=n_out, stream=s_)
 
-        lay.forward(n, stream=s, with_stats=with_stats, combine=combine)
+        lay.forward(n, stream=s, with_stats=with_stats, token_id=token_id, noise=noise, combine=combine)
         return x_out, n_out

@@ -253,3 +253,30 @@ def test_a_block_keeps_what_its_norms_gradients_take(rows, t):
     for key, sz in sizes.items():
         step = {"d_residual": 2.0 ** -8, "d_y": half}.get(key, U)
         assert (np.abs(_n(got[key]) - want[key]) <= (256 + t) * U * sz + step * np.abs(want[key]) + 1e-30).all(), key
+
+
+@pytest.mark.parametrize("routing", ["hash", "noisy", "uniform"])
+def test_a_block_over_the_other_routing_rules(routing):
+    """The rule's inputs reach the layer: the block equals its norm, the layer and the combine's norm."""
+    from routing_dispatch_expert_moe_b200 import moe as M
+    from routing_dispatch_expert_moe_b200.layer import MoEBlock, MoELayer, MoEWeights
+    g = torch.Generator(device="cuda").manual_seed(11)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    bf, t = torch.bfloat16, 50
+    w = MoEWeights(Wg=rnd(D, E) * 0.1, W_gu=(rnd(E, 2 * F, D) * 0.08).to(bf), W_dn=(rnd(E, D, F) * 0.08).to(bf),
+                   W_noise=rnd(D, E) * 0.1 if routing == "noisy" else None)
+    lay = MoELayer(w, K, 64, rows_dtype=bf, routing=routing)
+    blk = MoEBlock(lay, torch.ones(D, device="cuda"), torch.ones(D, device="cuda"))
+    r = rnd(t, D).to(bf)
+    extra = {"hash": dict(token_id=torch.arange(t, dtype=torch.int32, device="cuda")),
+             "noisy": dict(noise=rnd(t, E)), "uniform": {}}[routing]
+    x = blk.forward(r, **extra)[0].clone()
+    if extra:
+        with pytest.raises(ValueError, match="needs"):
+            blk.forward(r)
+    n = M.moe_block_norm(r, pre_weight=blk.pre_weight)[1]
+    lay.forward(n, **extra)
+    want = M.moe_combine_norm(r, lay.y_perm, lay.row_of[:t], lay.rows_max, post_weight=blk.post_weight)[0]
+    torch.cuda.synchronize()
+    assert M.moe_get_device_error() == 0
+    assert torch.equal(x, want)
