@@ -152,6 +152,9 @@ MOE_API int64_t moe_rows_max(int32_t T, int32_t E, int32_t k, int32_t capacity);
  * small operand), while the token-major one re-reads each row once per output tile.
  * Returns -1 for rows_max < 0 or E < 1.  Host only. */
 MOE_API int32_t moe_gate_up_weight_major(int64_t rows_max, int32_t E);
+/* The same for moe_expert_gate_up_i8 (weight-major below 192 rows); its gathered form is
+ * weight-major whatever the sizes. */
+MOE_API int32_t moe_gate_up_i8_weight_major(int64_t rows_max, int32_t E);
 
 /* ------------------------------------------------------------------------------------
  * moe_prepare_router_weight -- the tensor-core router's operand, made once at load time.

@@ -250,6 +250,7 @@ moe_status launch_prepare_fp4_scales(const uint8_t* scales, long long rows, int 
                                      cudaStream_t s);
 // Whether a grouped GEMM over E experts and rows_max rows takes the weight-major tiles.
 bool prefer_weight_major(long long rows_max, int E, bool down);
+bool prefer_weight_major_i8(long long rows_max, int E);       // gate/up
 
 moe_status launch_gate_up_tc(const void* x_rows, const int32_t* offsets, int E, int d, int F,
                              long long rows_max, const void* W_gu, void* h, cudaStream_t s);

@@ -850,9 +850,11 @@ constexpr long long kI8DownBelow = 144;
 // 31 / 24, 512 72 / 68, 2048 211 / 213.
 constexpr int kI8DownNarrow = 512;
 
+bool prefer_weight_major_i8(long long rows_max, int E) { return weight_major(rows_max / E < kI8GateUpBelow); }
+
 moe_status launch_gate_up_i8(const int8_t* x_q, const float* x_scale, const int32_t* offsets, int E, int d, int F,
                              long long rows_max, const int8_t* W, const float* w_scale, void* h, cudaStream_t s) {
-  if (weight_major(rows_max / E < kI8GateUpBelow))
+  if (prefer_weight_major_i8(rows_max, E))
     return launch_gate_up_wm_i8(x_q, x_scale, offsets, E, d, F, rows_max, W, w_scale, h, s);
   const int K = d / 2;
   CUtensorMap ma, mb;

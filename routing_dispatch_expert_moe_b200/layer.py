@@ -68,7 +68,8 @@ class MoELayer:
         fp32 buffer, rounded once to bf16 at the end when out_dtype is bf16).
         dispatch: "permute" (x_perm copy, then the GEMM), "gather" (the GEMM reads the
         token rows through token_of_row; same H bit for bit) or "auto" (gather where the
-        gate/up GEMM takes weight-major tiles, moe_gate_up_weight_major; permute otherwise).
+        gate/up GEMM takes weight-major tiles, moe_gate_up_weight_major or
+        moe_gate_up_i8_weight_major; permute otherwise).
         overlap: run the work nothing on the main path waits for (router statistics, and
         clearing y for the fused combine) on a second stream forked from and joined back
         to the caller's stream (one CUDA graph with two branches when captured).
@@ -124,7 +125,7 @@ class MoELayer:
             # gathered where the gate/up GEMM takes weight-major tiles (the token rows are its
             # small operand, read once either way); the permute copy otherwise
             if self.i8:
-                wm = self.rows_max // E < 192                     # where moe_expert_gate_up_i8 takes them
+                wm = M.moe_gate_up_i8_weight_major(self.rows_max, E)
             else:
                 wm = self.dtype == torch.bfloat16 and not self.fp4 and M.moe_gate_up_weight_major(self.rows_max, E)
             dispatch = "gather" if wm else "permute"

@@ -39,6 +39,7 @@ _SIGNATURES = {
     "moe_capacity": (_i32, [_i32, _i32, _i32, _f64, _i32]),
     "moe_rows_max": (_i64, [_i32, _i32, _i32, _i32]),
     "moe_gate_up_weight_major": (_i32, [_i64, _i32]),
+    "moe_gate_up_i8_weight_major": (_i32, [_i64, _i32]),
     "moe_route_workspace_bytes": (_size, [_i32, _i32, _i32]),
     "moe_router_weight_bytes": (_size, [_i32, _i32]),
     "moe_prepare_router_weight": (_i32, [_c_void_p, _i32, _i32, _c_void_p, _size, _c_void_p]),
@@ -211,7 +212,15 @@ def moe_gate_up_weight_major(rows_max: int, E: int) -> bool:
     """True when the bf16 gate/up GEMMs take weight-major tiles for these sizes."""
     r = int(lib().moe_gate_up_weight_major(rows_max, E))
     if r < 0:
-        raise MoEError(f"moe_gate_up_weight_major: invalid sizes rows_max={rows_max}, E={E}")
+        raise MoEError("moe_gate_up_weight_major", MOE_ERR_INVALID_ARG)
+    return bool(r)
+
+
+def moe_gate_up_i8_weight_major(rows_max: int, E: int) -> bool:
+    """True when moe_expert_gate_up_i8 takes weight-major tiles for these sizes."""
+    r = int(lib().moe_gate_up_i8_weight_major(rows_max, E))
+    if r < 0:
+        raise MoEError("moe_gate_up_i8_weight_major", MOE_ERR_INVALID_ARG)
     return bool(r)
 
 

@@ -280,3 +280,15 @@ def test_a_block_over_the_other_routing_rules(routing):
     torch.cuda.synchronize()
     assert M.moe_get_device_error() == 0
     assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("tiles,form", [("tokens", "permute"), ("weights", "gather")])
+def test_auto_dispatch_of_8_bit_experts_obeys_the_override(tiles, form, monkeypatch):
+    from routing_dispatch_expert_moe_b200 import moe as M
+    from routing_dispatch_expert_moe_b200.layer import MoELayer, MoEWeights
+    monkeypatch.setenv("MOE_B200_EXPERT_TILES", tiles)
+    w = MoEWeights(Wg=torch.randn(D, E, device="cuda"), W_gu=None, W_dn=None,
+                   W_gu_i8=M.quantize_experts_i8(torch.randn(E, 2 * F, D, device="cuda")),
+                   W_dn_i8=M.quantize_experts_i8(torch.randn(E, D, F, device="cuda")))
+    lay = MoELayer(w, k=K, T_max=64 if tiles == "tokens" else 2048, dispatch="auto")   # 16 and 512 rows an expert
+    assert lay.dispatch_mode == form

@@ -30,3 +30,20 @@ def test_sizes_at_the_limits(L):
     for T in (1, 7, 5000, (1 << 24) - 1):
         for d in (8, 16, 256, 264, 2048, 8192):
             assert f(T, d) > 0 and f(T, d) % (16 * d) == 0               # four fp32 rows a block
+
+
+def test_gate_up_i8_orientation_query(L, monkeypatch):
+    """Weight-major tiles below 192 rows an expert on average; the override variable wins, as in the
+    GEMMs and in the layer's choice of its dispatch."""
+    from routing_dispatch_expert_moe_b200 import moe as M
+    monkeypatch.delenv("MOE_B200_EXPERT_TILES", raising=False)
+    f = M.moe_gate_up_i8_weight_major
+    assert f(191, 1) and not f(192, 1) and f(0, 8) and f(192 * 64 - 1, 64) and not f(192 * 64, 64)
+    for query in (f, M.moe_gate_up_weight_major):
+        for bad in ((-1, 8), (10, 0)):
+            with pytest.raises(M.MoEError):
+                query(*bad)
+    monkeypatch.setenv("MOE_B200_EXPERT_TILES", "tokens")
+    assert not f(1, 1)
+    monkeypatch.setenv("MOE_B200_EXPERT_TILES", "weights")
+    assert f(1 << 20, 1)
