@@ -222,3 +222,63 @@ def test_full_softmax_gates_are_within_the_stated_bound(T, E, k, G, kept, spread
             assert err.max() <= 121 * U
             if spread == 0.0 and bias is not None:
                 assert err.max() <= U * 1.001               # rounded once
+
+
+# ---------------------------------------------------------------- the 8-bit products
+@pytest.mark.parametrize("call", ["gate_up", "gather", "down"])
+@pytest.mark.parametrize("tiles", ["tokens", "weights"])
+def test_bad_offsets_between_good_experts(call, tiles, monkeypatch):
+    """Two entries out of the buffer: the experts on both sides of each are skipped and recorded, all
+    others' rows are right, and nothing else is written.  More tiles than CTA pairs, empty experts
+    among them, so that every role walks past the gaps."""
+    M = _M()
+    monkeypatch.setenv("MOE_B200_EXPERT_TILES", tiles)
+    d, F, E = (256, 1040, 60) if call != "down" else (1040, 640, 60)
+    rng = np.random.default_rng(3)
+    counts = rng.integers(0, 40, E)
+    counts[[0, 7, 8, 30, E - 1]] = [3, 0, 300, 0, 17]
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rows = int(off[-1])
+    N, K = (2 * F, d) if call != "down" else (d, F)
+    T = 50 if call == "gather" else rows
+    q = rng.integers(-127, 128, (T, K)).astype(np.int8)
+    scale = ((rng.random(T) + 0.5) * 1e-2).astype(np.float32)
+    W = rng.integers(-127, 128, (E, N, K)).astype(np.int8)
+    ws = ((rng.random((E, N)) + 0.5) * (2e-2 / np.sqrt(K))).astype(np.float32)
+    tok = rng.integers(0, T, rows).astype(np.int32) if call == "gather" else None
+    bad = off.copy()
+    bad[12], bad[41] = rows + 50, -3
+    c = lambda a: torch.from_numpy(a).cuda()
+    out = torch.full((rows, F if call != "down" else d), 7.0, dtype=torch.bfloat16, device="cuda")
+    if call == "down":
+        M.moe_expert_down_i8(c(q), c(scale), c(bad), c(W), c(ws), rows, y_rows=out)
+    else:
+        M.moe_expert_gate_up_i8(c(q), c(scale), c(bad), c(W), c(ws), rows, out, None if tok is None else c(tok))
+    torch.cuda.synchronize()
+    assert M.moe_get_device_error() == 3
+    rq, rs = (q, scale) if tok is None else (q[tok], scale[tok])
+    want = (B.down_i8 if call == "down" else B.gate_up_i8)(rq, rs, off, W, ws)
+    for e in (11, 12, 40, 41):
+        want[off[e]:off[e + 1]] = 7.0
+    tol = 4 * U + 2.0 ** -8 if call == "down" else 2.0 ** -8 + 2.0 ** -17
+    assert (np.abs(out.double().cpu().numpy() - want) <= np.abs(want) * tol + 1e-30).all()
+
+
+@pytest.mark.parametrize("tiles", ["tokens", "weights"])
+def test_more_rows_than_any_tile_and_most_experts_empty(tiles, monkeypatch):
+    """896 experts of which five have rows: the walk to the next tile's expert passes hundreds."""
+    M = _M()
+    monkeypatch.setenv("MOE_B200_EXPERT_TILES", tiles)
+    E, d, F = 896, 128, 272
+    counts = np.zeros(E, np.int64)
+    counts[[0, 3, 400, 894, 895]] = [1, 700, 257, 5, 130]
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rows = int(off[-1])
+    rng = np.random.default_rng(5)
+    q, scale = rng.integers(-127, 128, (rows, d)).astype(np.int8), (rng.random(rows) * 0.05).astype(np.float32)
+    W, ws = rng.integers(-127, 128, (E, 2 * F, d)).astype(np.int8), (rng.random((E, 2 * F)) * 1e-3).astype(np.float32)
+    c = lambda a: torch.from_numpy(a).cuda()
+    h = M.moe_expert_gate_up_i8(c(q), c(scale), c(off), c(W), c(ws), rows)
+    _ok()
+    want = B.gate_up_i8(q, scale, off, W, ws)
+    assert (np.abs(h.double().cpu().numpy() - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -17) + 1e-30).all()
