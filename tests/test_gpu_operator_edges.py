@@ -63,6 +63,55 @@ def test_column_sums_of_calls_that_share_a_workspace():
             assert torch.equal(t, want[i % 2][key]), (i, key)
 
 
+def _norm_bars(v, x, y, post, gate, pre, alpha, eps=1e-6):
+    """Sizes of the terms of each gradient, as in the norms' own tests."""
+    T, d = x.shape
+    u, out = np.abs(v["d_x"]), {}
+    if pre is not None:
+        rx = 1.0 / np.sqrt((x * x).mean(1, keepdims=True) + eps)
+        g, xh = np.abs(v["d_n"] * pre), np.abs(x * rx)
+        out["d_pre_weight"] = (np.abs(v["d_n"]) * xh).sum(0)
+        u = u + rx * (g + xh * (g * xh).mean(1, keepdims=True))
+    yr = 1.0 / np.sqrt((y * y).mean(1, keepdims=True) + eps)
+    b = np.abs(y * yr * post)
+    out["d_residual"] = abs(alpha) * u
+    out["d_gate"] = (u * b).reshape(gate.shape[0], -1, d).sum(1)
+    ug = u * np.repeat(np.abs(gate), T // gate.shape[0], axis=0)
+    out["d_post_weight"] = (ug * np.abs(y * yr)).sum(0)
+    h, yh = ug * np.abs(post), np.abs(y * yr)
+    out["d_y"] = yr * (h + yh * (h * yh).mean(1, keepdims=True))
+    return out
+
+
+@pytest.mark.parametrize("T,d,G", [(450, 8192, 3), (300, 7168, 300), (450, 5736, 1), (1500, 2048, 5), (900, 4096, 2),
+                                   (900, 4088, 9), (1800, 1112, 4), (2400, 520, 6)])
+@pytest.mark.parametrize("yt,rt,nt", [("bf16", "bf16", "bf16"), ("f32", "f32", "f32"), ("bf16", "f32", "bf16")])
+@pytest.mark.parametrize("with_pre", [True, False])
+def test_norm_gradients_of_several_rows_a_block(T, d, G, yt, rt, nt, with_pre):
+    """More tokens than blocks: the ring of one to four rows turns over, and gate groups end inside a
+    block's run and span several."""
+    M = _M()
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}
+    g = torch.Generator(device="cuda").manual_seed(T + d)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    v = dict(d_x=(rnd(T, d) * 0.1).to(dt[rt]), d_n=(rnd(T, d) * 0.1).to(dt[nt]) if with_pre else None,
+             x_out=rnd(T, d).to(dt[rt]), y=(rnd(T, d) * 0.3).to(dt[yt]))
+    post, pre, gate = rnd(d), rnd(d) if with_pre else None, rnd(G, d)
+    got = M.moe_block_norm_backward(**v, post_weight=post, gate=gate, alpha=0.5, pre_weight=pre)
+    again = M.moe_block_norm_backward(**v, post_weight=post, gate=gate, alpha=0.5, pre_weight=pre)
+    _ok()
+    n = {k: None if t is None else t.double().cpu().numpy() for k, t in v.items()}
+    p = [None if t is None else t.double().cpu().numpy() for t in (post, gate, pre)]
+    want = B.block_norm_backward(n["d_x"], n["d_n"], n["x_out"], n["y"], p[0], p[1], 0.5, p[2])
+    half = {"d_residual": 2.0 ** -8 if rt == "bf16" else U, "d_y": 2.0 ** -8 if yt == "bf16" else U}
+    for key, size in _norm_bars(n, n["x_out"], n["y"], p[0], p[1], p[2], 0.5).items():
+        assert torch.equal(got[key], again[key]), key
+        err = np.abs(got[key].double().cpu().numpy() - want[key])
+        # rows: 256 roundings; column sums: one more for each token
+        terms = 256 + (0 if key in half else T)
+        assert (err <= terms * U * size + half.get(key, U) * np.abs(want[key]) + 1e-30).all(), key
+
+
 # ---------------------------------------------------------------- the routing's gradient
 def _score64(l, score):
     """Score and derivative in 64 bits, without a difference of near numbers; 0 where masked."""
