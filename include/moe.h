@@ -723,7 +723,11 @@ MOE_API moe_status moe_expert_down_fp4(const void* h, const int32_t* offsets, in
  * A logit of -inf or NaN masks its expert: its key is -inf whatever its bias, it adds
  * nothing to its group, and its gate is 0 where it is selected all the same (fewer than k
  * unmasked experts in the kept groups); a token with every expert masked has gates 0.
- * A logit of +inf counts as the largest float.
+ * A logit of +inf counts as the largest float.  A bias of -inf or NaN gives its expert the key -inf
+ * and nothing to add to its group.
+ * A token of which more than 32 experts stay in question in fp32 (many equal keys), and every token
+ * if a bias is infinite or NaN, is taken in fp64 throughout, which costs it some 15 times as much; to
+ * switch an expert off for all tokens, a logit of -inf is the cheap way.
  * Errors: INVALID_ARG for a null pointer, T < 0, k < 1, n_groups < 1, groups_kept outside
  * [1, n_groups], E not a multiple of n_groups, k > groups_kept * n, an unknown score or
  * group_score, renormalize not 0/1 or a non-finite scale; UNSUPPORTED for E > 1024, k > 32
@@ -750,8 +754,9 @@ MOE_API moe_status moe_route_grouped(const float* logits, const float* select_bi
  * expert a token names twice takes the sum of both slots' gradients, in slot order.  A topk_idx
  * entry outside [0, E) records MOE_DEVERR_EXPERT_ID and its slot is left out.
  * Gradients are taken in fp32; what is divided by a sum of scores keeps its relative precision where
- * the scores are too small for fp32.  Scores below e^-745 (fp64's least) count as 0, as in
- * moe_route_grouped; a sigmoid that is not divided counts as 0 below 2^-126.
+ * all of those are too small for fp32.  Scores below e^-745 (fp64's least) count as 0, as in
+ * moe_route_grouped; a score that is not divided, or stands beside one above e^-40, counts as 0
+ * below 2^-126.
  * Errors: INVALID_ARG for a null logits or d_logits, one of topk_idx / d_gate without the
  * other, aux_coef != 0 without load, T < 0, k < 1 or k > E with a selection, an unknown
  * score, renormalize not 0/1 or a non-finite scale or coefficient; UNSUPPORTED for E > 1024

@@ -25,7 +25,9 @@
 // blocks' partial sums in a fixed order (results repeat bit for bit).  8192 tokens, d = 2048:
 // 47 us with the sums, where the bytes need 31: two block-wide sums a row, half the issue rate.
 // 4096 tokens, d = 7168, fp32 residual: 104 us (110 with pre read through the first-level cache),
-// where the bytes need 81.
+// where the bytes need 81.  Where shared memory holds one row's inputs only, its loads wait for the
+// row before: fp32 residual, 8192 x 2048 67 us (46), 4096 x 4096 70 (46), 4096 x 8192 135 (92); all
+// fp32 82 (61), 90 (61) and 178 (123).
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "tc_prims.cuh"
@@ -118,6 +120,9 @@ struct NormArgs {
 };
 
 // YT: y or the expert rows; RT: the residual stream; NT: the normed rows.
+// V = 1: five blocks, 51 registers; fp32 expert rows (32 bytes a load, four in flight) spill some of
+// them (84 to 100 bytes): 8192 tokens, d = 2048, k = 8, 116 us where the bytes need 97, as near as the
+// bf16 rows' 68 to 56.
 template <typename YT, typename RT, typename NT, int V, bool COMBINE>
 __global__ void __launch_bounds__(V == 1 ? 256 : 512, V == 1 ? 5 : 1)
 block_norm_kernel(const NormArgs a) {
@@ -286,7 +291,8 @@ __device__ __forceinline__ void bulk_row(uint32_t dst, const void* src, uint32_t
 // stay in registers.  A buffer is filled again once every thread is past the row after it (the
 // barrier of that row's first reduction), or, with one buffer, past the row itself.
 // gate * post of the current gate group and pre wait in shared memory (each thread its own columns):
-// the rows leave little of the first-level cache for them.
+// the rows leave little of the first-level cache for them.  pre costs some widths a stage (with an
+// fp32 residual and bf16 y and n: 8192 two to one), and gains at others (4096 x 7168: 110 -> 105 us).
 template <typename YT, typename RT, typename NT, int V>
 __global__ void __launch_bounds__(V == 1 ? 64 : 512, V == 1 ? 12 : 1)
 block_norm_grad_kernel(const NormGradArgs a) {

@@ -835,8 +835,11 @@ moe_status launch_gate_up_gather_tc(const void* x, const int32_t* token_of_row, 
 // the same tiles as rows of K / 2 two-byte elements (K a multiple of 16); the accumulators are
 // exact int32 sums and the epilogue multiplies them by the row's and the column's scale.  A k-block
 // holds twice the products of a bf16 one, so the epilogue has half the time: CTA pairs with eight
-// epilogue warps here, and weight-major tiles for small groups, for the down GEMM too.  Gate/up of 64 experts, 65,536 rows, d = 2048, F = 1024: 211 us (5.5e11 operations, 0.78 of twice
-// the bf16 burst rate), the tensor pipe busy 0.77 of it. ----
+// epilogue warps here, and weight-major tiles for small groups, for the down GEMM too.  Gate/up of
+// 64 experts, 65,536 rows, d = 2048, F = 1024: 211 us (5.5e11 operations, 0.78 of twice the bf16
+// burst rate), the tensor pipe busy 0.77 of it; 270 in a long run of calls, where the power cap holds
+// the clock at some 1250 MHz.  Down of 64 experts, 512 rows each, d = 4096, F = 2048: 228 us for bf16
+// rows and 260 for fp32 ones, where the products need 166 and the bytes 133 and 174. ----
 
 // Weight-major below so many rows an expert on average.  Gate/up, tokens against weights (us):
 // d = 4096, F = 2048, 64 experts: 64 rows 230 / 168, 128 234 / 214, 192 279 / 265, 256 301 / 353,

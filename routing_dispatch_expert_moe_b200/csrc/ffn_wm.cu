@@ -1079,7 +1079,8 @@ moe_status launch_down_wm(const void* h, const int32_t* offsets, int E, int d, i
 
 // 8-bit rows and weights, weight-major: the same tiles over rows of K / 2 two-byte elements.
 // Gate/up of 64 experts with 2 rows each, d = 2048, F = 1024: 49 us, 5.4 TB/s of weights.  Down of
-// 896 experts, 131,072 rows, d = 7168, F = 256: 739 us for 3.6 GB, 0.74 of the copy rate.
+// 896 experts, 131,072 rows, d = 7168, F = 256: 700 us for 3.5 GB, 0.77 of the copy rate; 807 in a long
+// run of calls, where the power cap holds the clock at 1570 MHz.
 moe_status launch_gate_up_wm_i8(const int8_t* x_q, const float* x_scale, const int32_t* offsets, int E, int d, int F,
                                 long long rows_max, const int8_t* W, const float* w_scale, void* h, cudaStream_t s) {
   CUtensorMap mw, mx;

@@ -122,7 +122,9 @@ struct GroupArgs {
 
 // The whole selection of one token in fp64, by the warp.  A lane keeps the keys of its part of its
 // group (every team-th expert) in local memory and its best one at hand; k rounds of an arg-max
-// over the lanes follow.  One token here holds up its warp for some 15 us.
+// over the lanes follow.  One token here holds up its warp for some 15 us; 32768 tokens of 896 experts
+// that all come here take 1.3 to 1.45 ms in place of 98 us (a router at its zero start, or an infinite
+// or NaN bias).
 template <int SCORE>
 __device__ __noinline__ Pick route_token_fp64(const GroupArgs& a, const float* __restrict__ l) {
   const int lane = threadIdx.x & 31;
